@@ -1,5 +1,7 @@
 /*
- * vit_decoder.h -- C ABI of the two decoder-side steps that consume the vision encoder's output.
+ * vit_decoder.h -- C ABI of the decoder-side steps around the vision encoder's output: the position
+ * rotation (alone, or with the per-head norms of q and k), the input rows, their gradients, and
+ * attention over a prompt that a batch of sequences shares.
  *
  * What they compute (the passages that define them):
  *   - mrope_apply: "Qwen2-VL" (ZeroModels Keras docs), intro (the decoder's rotary embedding is split
@@ -10,6 +12,8 @@
  *   - scatter_vision_tokens: "Qwen2-VL (Native-Resolution VLM)", Structure table rows 6-10 (merged
  *     image tokens and embedded text tokens form one sequence of the decoder's width); "Qwen2-VL",
  *     several images in one conversation (each marker expands to its image's own token count).
+ *   - mrope_norm_apply, embed_vision_tokens, prefix_attention: no counterpart on the pages beyond the
+ *     above; the formulas stand at each declaration.
  *
  * Conventions as in vit.h: device pointers unless marked HOST, bf16 row-major, asynchronous on
  * `stream`, argument errors returned before any launch, data errors written to dev_status.
@@ -22,6 +26,11 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* Element types of the calls that take one. */
+#define VIT_DTYPE_BF16 0
+#define VIT_DTYPE_F16  1   /* IEEE half */
+#define VIT_DTYPE_F32  2
 
 /* 3-D M-RoPE, in place. q: bf16 [L, n_heads, head_dim], k: bf16 [L, n_kv_heads, head_dim] (either
  * may be NULL with its head count 0); pos: int32 [3, L], the (t, h, w) ids mrope_index writes.
@@ -44,6 +53,102 @@ int mrope_apply(void *q, int n_heads, void *k, int n_kv_heads, int head_dim, con
  * no-op that reads no pointer. */
 int scatter_vision_tokens(const int32_t *input_ids, int64_t L, const void *embed_table, int64_t vocab, int dim,
                           const void *vision, int64_t n_vision, void *out, int32_t *dev_status, void *stream);
+
+/* Per-head RMS norm of q and k and 3-D M-RoPE in one pass. For each head vector x of head_dim values:
+ * n = x / sqrt(mean(x^2) + eps) * w, then n turned exactly as by mrope_apply (pos, theta, sections as
+ * there). q: [L, n_heads, head_dim] with heads contiguous and q_stride elements from token to token (a
+ * slice of a packed QKV product, for example), q_out likewise; k the same; either may be NULL with its
+ * head count 0. An output may be its own input (same pointer and stride); otherwise outputs overlap
+ * neither input. q_w, k_w: [head_dim] of the same type, or NULL (ones). dtype: VIT_DTYPE_*, of q, k,
+ * weights and outputs alike. Sums, norm and turn in fp32 (angles in double precision), rounded once.
+ * Pointers 16-byte aligned and strides multiples of 16 bytes (VIT_ERR_ALIGN); strides at least heads *
+ * head_dim; eps > 0; other limits as mrope_apply. */
+int mrope_norm_apply(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int n_heads, const void *k,
+                     int64_t k_stride, void *k_out, int64_t k_out_stride, int n_kv_heads, int head_dim, int dtype,
+                     const void *q_w, const void *k_w, float eps, const int32_t *pos, int64_t L, double theta,
+                     const int32_t *sections, void *stream);
+
+/* Gradient of mrope_norm_apply. dq_out, dk_out: the gradients of its outputs (strides dq_out_stride,
+ * dk_out_stride); q, k, weights, positions as given to it (its outputs are not needed). Writes dq, dk
+ * (same type; dq may be dq_out or q with the same stride, k likewise) and, where not NULL, dq_w and
+ * dk_w: fp32 [head_dim], the sums over tokens and heads (overwritten; zeros for L = 0), in a fixed
+ * order, so equal inputs give equal bits. A NULL weight still gives its gradient (taken at ones).
+ * workspace: mrope_norm_grad_workspace(head_dim) bytes of device memory, 16-byte aligned, not shared
+ * with work that may run at the same time; NULL is allowed when both weight gradients are. */
+int64_t mrope_norm_grad_workspace(int head_dim);
+int mrope_norm_grad(const void *dq_out, int64_t dq_out_stride, const void *q, int64_t q_stride, void *dq,
+                    int64_t dq_stride, int n_heads, const void *dk_out, int64_t dk_out_stride, const void *k,
+                    int64_t k_stride, void *dk, int64_t dk_stride, int n_kv_heads, int head_dim, int dtype,
+                    const void *q_w, const void *k_w, float *dq_w, float *dk_w, float eps, const int32_t *pos,
+                    int64_t L, double theta, const int32_t *sections, void *workspace, int64_t workspace_bytes,
+                    void *stream);
+
+/* scatter_vision_tokens with a scale and a choice of types: out[i] = scale * embed_table[input_ids[i]]
+ * (in fp32, rounded once) for text, vision[k] unscaled for the k-th placeholder. All of one dtype
+ * (VIT_DTYPE_*). Arguments, limits and data errors as scatter_vision_tokens; scale finite. */
+int embed_vision_tokens(const int32_t *input_ids, int64_t L, const void *embed_table, int dtype, int64_t vocab,
+                        int dim, float scale, const void *vision, int64_t n_vision, void *out, int32_t *dev_status,
+                        void *stream);
+
+/* Gradient of embed_vision_tokens. d_out: [L, dim] of dtype. d_table: [vocab, dim] of table_dtype (dtype
+ * or VIT_DTYPE_F32): d_table[v] = scale * sum of d_out[i] over the text positions i with id v, summed in
+ * fp32 in a fixed order (equal inputs give equal bits) and rounded once; accumulate = 0 writes the
+ * whole table, zeros in the rows no token names; accumulate != 0 adds to what is there and touches only
+ * the rows named. d_vision: [n_vision, dim] of dtype, the placeholders' rows (may be NULL with n_vision 0). Data
+ * errors (placeholder count != n_vision, ids outside [0, vocab)) write VIT_ERR_TOKENS to dev_status;
+ * such positions add nothing, and vision tokens without a placeholder get zeros. L <= 2^18, vocab <=
+ * 2^30, dim a multiple of 8 up to 65536; pointers 16-byte aligned. workspace:
+ * embed_vision_tokens_grad_workspace(L, vocab, dim) bytes (0 for sizes out of range) of device memory, 16-byte aligned, not shared
+ * with work that may run at the same time; L = 0 is allowed (zeros, or nothing when accumulating). */
+int64_t embed_vision_tokens_grad_workspace(int64_t L, int64_t vocab, int dim);
+int embed_vision_tokens_grad(const int32_t *input_ids, int64_t L, const void *d_out, int dtype, int64_t vocab, int dim,
+                             float scale, void *d_table, int table_dtype, int accumulate, void *d_vision,
+                             int64_t n_vision, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                             void *stream);
+
+/* Attention of a batch of sequences that share a prefix of keys (an image's or a video's tokens and
+ * the prompt around them), each with keys of its own behind it. For query j of sequence b and head h
+ * (key-value head h / (n_heads / n_kv_heads)):
+ *   out = softmax(scale * q . key) value   over all prefix keys and the own keys s < lens[b], with
+ *   causal != 0 only s <= lens[b] - n_q(b) + j: the last query sees all own keys (its own among them).
+ * A row that sees no key gives zeros and lse = -inf. lse = log(sum exp(scale * q . key)).
+ * Strides are in elements, multiples of 8; a head's head_dim values are contiguous. A value of an own
+ * key at or behind lens[b] is never used, whatever the memory holds; a key inside lens[b] that a
+ * causal row may not see must still be finite. */
+typedef struct {
+    int dtype;                       /* VIT_DTYPE_BF16 or VIT_DTYPE_F16: q, keys, values, out         */
+    int n_heads, n_kv_heads;         /* n_heads a multiple of n_kv_heads, at most 128 times as many   */
+    int head_dim;                    /* a multiple of 8, 8..128                                       */
+    float scale;                     /* positive; 1 / sqrt(head_dim) as a rule                        */
+    int causal;
+    const void *q;                   /* [total_q, n_heads, head_dim], heads contiguous                */
+    int64_t q_stride;                /* from token to token                                           */
+    void *out;                       /* as q, no overlap with any input                               */
+    int64_t out_stride;
+    float *lse;                      /* fp32 [total_q, n_heads] or NULL                               */
+    int64_t total_q;                 /* total_q * n_heads < 2^31                                      */
+    int64_t max_q;                   /* no sequence has more queries                                  */
+    const int32_t *cu_q;             /* [n_seq + 1] first row of each sequence's queries, from 0, or
+                                        NULL: max_q each. Rows from cu_q[n_seq] on are left alone     */
+    int n_seq;                       /* 1..65536                                                      */
+    const void *prefix_k, *prefix_v; /* [prefix_len, n_kv_heads, head_dim], NULL with prefix_len 0    */
+    int64_t prefix_len;              /* 0..2^30                                                       */
+    int64_t prefix_k_token, prefix_k_head, prefix_v_token, prefix_v_head;
+    const void *k, *v;               /* [n_seq, >= max_len, n_kv_heads, head_dim], or both NULL       */
+    int64_t k_seq, k_token, k_head, v_seq, v_token, v_head;
+    const int32_t *lens;             /* [n_seq] own keys of each sequence (device), with k            */
+    int64_t max_len;                 /* no length is above this; 0 without k                          */
+} prefix_attention_desc;
+
+/* workspace: prefix_attention_workspace(desc) bytes (host-only; 0 for a bad descriptor) of device
+ * memory, 16-byte aligned, not shared with work that may run at the same time; it depends on sizes
+ * alone, not on what cu_q and lens hold. Data errors (a length outside [0, max_len], query ranges that
+ * leave [0, total_q] or are longer than max_q) write VIT_ERR_LIMIT to dev_status (int32 [1] device, or
+ * NULL); the values are clamped, nothing outside the buffers is touched, and the rows concerned
+ * are not meaningful. A kernel wait that timed out writes VIT_ERR_TIMEOUT there. */
+int64_t prefix_attention_workspace(const prefix_attention_desc *desc);
+int prefix_attention(const prefix_attention_desc *desc, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                     void *stream);
 
 #ifdef __cplusplus
 }

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cmath>
 #include <cstring>
 #include <memory>
 #include <mutex>
@@ -813,6 +814,172 @@ int scatter_vision_tokens(const int32_t *input_ids, int64_t L, const void *embed
     if (!aligned16(embed_table) || !aligned16(out) || (vision && !aligned16(vision))) return VIT_ERR_ALIGN;
     return vith::scatter_launch(input_ids, L, embed_table, vocab, dim, vision, n_vision, out, dev_status,
                                 static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+int elem_bytes(int dtype) { return dtype == VIT_DTYPE_F32 ? 4 : 2; }
+bool known_dtype(int dtype) { return dtype == VIT_DTYPE_BF16 || dtype == VIT_DTYPE_F16 || dtype == VIT_DTYPE_F32; }
+
+// one operand of the norm / rotation calls: pointer and token stride of [L, heads, head_dim]
+int check_rows(const void *p, int64_t stride, int heads, int head_dim, int dtype) {
+    if (!p || stride < int64_t(heads) * head_dim || stride > (int64_t(1) << 40)) return VIT_ERR_ARG;
+    if (!aligned16(p) || stride * elem_bytes(dtype) % 16) return VIT_ERR_ALIGN;
+    return VIT_OK;
+}
+
+// sizes of the norm / rotation calls (weights, positions and sections)
+int check_norm(int n_heads, int n_kv_heads, int head_dim, int dtype, const void *q_w, const void *k_w, float eps,
+               const int32_t *pos, int64_t L, double theta, const int32_t *sections) {
+    if ((L != 0 && !pos) || !sections || L < 0 || L > (int64_t(1) << 31) - 1 || !(theta > 1.0) || !(eps > 0.0f))
+        return VIT_ERR_ARG;
+    if (!known_dtype(dtype) || head_dim < 16 || head_dim > 256 || head_dim % 16) return VIT_ERR_ARG;
+    if (n_heads < 0 || n_kv_heads < 0 || n_heads > 65536 / head_dim || n_kv_heads > 65536 / head_dim) return VIT_ERR_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (sections[i] < 0 || sections[i] > head_dim / 2) return VIT_ERR_ARG;
+    if (sections[0] + sections[1] + sections[2] != head_dim / 2) return VIT_ERR_ARG;
+    if ((q_w && !aligned16(q_w)) || (k_w && !aligned16(k_w))) return VIT_ERR_ALIGN;
+    return VIT_OK;
+}
+
+bool embed_sizes_ok(int64_t L, int64_t vocab, int dim) {
+    return L >= 0 && L <= (int64_t(1) << 18) && vocab >= 1 && vocab <= (int64_t(1) << 30) && dim >= 8 && dim <= 65536 &&
+           dim % 8 == 0;
+}
+
+// one of the key / value operands of prefix_attention; seq stride -1: none
+int check_keys(const void *p, int64_t token, int64_t head, int64_t seq, int head_dim) {
+    const int64_t most = int64_t(1) << 38;
+    if (!p || token < head_dim || head < head_dim || token > most || head > most) return VIT_ERR_ARG;
+    if (seq >= 0 && (seq < head_dim || seq > most)) return VIT_ERR_ARG;
+    if (!aligned16(p) || token % 8 || head % 8 || (seq >= 0 && seq % 8)) return VIT_ERR_ALIGN;
+    return VIT_OK;
+}
+
+int check_prefix(const prefix_attention_desc *d) {
+    if (!d || (d->dtype != VIT_DTYPE_BF16 && d->dtype != VIT_DTYPE_F16)) return VIT_ERR_ARG;
+    if (d->head_dim < 8 || d->head_dim > 128 || d->head_dim % 8) return VIT_ERR_ARG;
+    if (d->n_kv_heads < 1 || d->n_heads < 1 || d->n_heads % d->n_kv_heads || d->n_heads / d->n_kv_heads > 128)
+        return VIT_ERR_ARG;
+    if (!std::isfinite(d->scale) || !(d->scale > 0.0f) || d->n_seq < 1 || d->total_q < 0 || d->max_q < 1 || d->prefix_len < 0 || d->max_len < 0)
+        return VIT_ERR_ARG;
+    if (d->n_seq > 65536 || d->n_heads > 65536 || d->prefix_len > (int64_t(1) << 30) || d->max_len > (int64_t(1) << 30))
+        return VIT_ERR_LIMIT;
+    if (d->total_q > ((int64_t(1) << 31) - 1) / d->n_heads || d->max_q > ((int64_t(1) << 31) - 1) / d->n_heads / d->n_seq)
+        return VIT_ERR_LIMIT;
+    if (!d->cu_q && d->total_q != 0 && d->total_q != d->max_q * d->n_seq) return VIT_ERR_ARG;
+    if (!d->k != !d->v || !d->k != !d->lens || (!d->k && d->max_len != 0)) return VIT_ERR_ARG;
+    if (d->total_q > 0 && (!d->q || !d->out)) return VIT_ERR_ARG;
+    const int64_t width = int64_t(d->n_heads) * d->head_dim, most = int64_t(1) << 38;
+    if (d->q_stride < width || d->out_stride < width || d->q_stride > most || d->out_stride > most) return VIT_ERR_ARG;
+    if (d->q_stride % 8 || d->out_stride % 8 || (d->q && !aligned16(d->q)) || (d->out && !aligned16(d->out)))
+        return VIT_ERR_ALIGN;
+    int rc = VIT_OK;
+    if (d->prefix_len > 0) {
+        rc = check_keys(d->prefix_k, d->prefix_k_token, d->prefix_k_head, -1, d->head_dim);
+        if (rc == VIT_OK) rc = check_keys(d->prefix_v, d->prefix_v_token, d->prefix_v_head, -1, d->head_dim);
+    }
+    if (rc == VIT_OK && d->k) {
+        if (d->k_seq < 0 || d->v_seq < 0) return VIT_ERR_ARG;
+        rc = check_keys(d->k, d->k_token, d->k_head, d->k_seq, d->head_dim);
+        if (rc == VIT_OK) rc = check_keys(d->v, d->v_token, d->v_head, d->v_seq, d->head_dim);
+    }
+    return rc;
+}
+
+}  // namespace
+
+int mrope_norm_apply(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int n_heads, const void *k,
+                     int64_t k_stride, void *k_out, int64_t k_out_stride, int n_kv_heads, int head_dim, int dtype,
+                     const void *q_w, const void *k_w, float eps, const int32_t *pos, int64_t L, double theta,
+                     const int32_t *sections, void *stream) {
+    int rc = check_norm(n_heads, n_kv_heads, head_dim, dtype, q_w, k_w, eps, pos, L, theta, sections);
+    if (rc != VIT_OK || L == 0) return rc;
+    vith::NormRopeCall c{{q, k}, {q_out, k_out}, {}, {q_w, k_w}, {q_stride, k_stride}, {q_out_stride, k_out_stride},
+                         {}, {n_heads, n_kv_heads}, head_dim, dtype, eps, pos, L, theta, sections};
+    for (int i = 0; i < 2 && rc == VIT_OK; ++i) {
+        if (c.heads[i] == 0) continue;
+        rc = check_rows(c.x[i], c.x_stride[i], c.heads[i], head_dim, dtype);
+        if (rc == VIT_OK) rc = check_rows(c.y[i], c.y_stride[i], c.heads[i], head_dim, dtype);
+        if (rc == VIT_OK && c.x[i] == c.y[i] && c.x_stride[i] != c.y_stride[i]) rc = VIT_ERR_ARG;
+    }
+    return rc != VIT_OK ? rc : vith::norm_rope_launch(c, static_cast<cudaStream_t>(stream));
+}
+
+int64_t mrope_norm_grad_workspace(int head_dim) {
+    return head_dim < 16 || head_dim > 256 ? 0 : vith::norm_rope_grad_workspace(head_dim);
+}
+
+int mrope_norm_grad(const void *dq_out, int64_t dq_out_stride, const void *q, int64_t q_stride, void *dq,
+                    int64_t dq_stride, int n_heads, const void *dk_out, int64_t dk_out_stride, const void *k,
+                    int64_t k_stride, void *dk, int64_t dk_stride, int n_kv_heads, int head_dim, int dtype,
+                    const void *q_w, const void *k_w, float *dq_w, float *dk_w, float eps, const int32_t *pos,
+                    int64_t L, double theta, const int32_t *sections, void *workspace, int64_t workspace_bytes,
+                    void *stream) {
+    int rc = check_norm(n_heads, n_kv_heads, head_dim, dtype, q_w, k_w, eps, pos, L, theta, sections);
+    if (rc != VIT_OK) return rc;
+    vith::NormRopeCall c{{q, k}, {dq, dk}, {dq_out, dk_out}, {q_w, k_w}, {q_stride, k_stride}, {dq_stride, dk_stride},
+                         {dq_out_stride, dk_out_stride}, {n_heads, n_kv_heads}, head_dim, dtype, eps, pos, L, theta,
+                         sections};
+    for (int i = 0; i < 2 && L > 0; ++i) {
+        if (c.heads[i] == 0) continue;
+        rc = check_rows(c.x[i], c.x_stride[i], c.heads[i], head_dim, dtype);
+        if (rc == VIT_OK) rc = check_rows(c.y[i], c.y_stride[i], c.heads[i], head_dim, dtype);
+        if (rc == VIT_OK) rc = check_rows(c.dy[i], c.dy_stride[i], c.heads[i], head_dim, dtype);
+        if (rc == VIT_OK && ((c.x[i] == c.y[i] && c.x_stride[i] != c.y_stride[i]) ||
+                             (c.dy[i] == c.y[i] && c.dy_stride[i] != c.y_stride[i])))
+            rc = VIT_ERR_ARG;
+        if (rc != VIT_OK) return rc;
+    }
+    if ((dq_w || dk_w) && (!workspace || workspace_bytes < vith::norm_rope_grad_workspace(head_dim))) return VIT_ERR_ARG;
+    if ((dq_w || dk_w) && !aligned16(workspace)) return VIT_ERR_ALIGN;
+    return vith::norm_rope_grad_launch(c, dq_w, dk_w, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int embed_vision_tokens(const int32_t *input_ids, int64_t L, const void *embed_table, int dtype, int64_t vocab,
+                        int dim, float scale, const void *vision, int64_t n_vision, void *out, int32_t *dev_status,
+                        void *stream) {
+    if (!known_dtype(dtype) || !std::isfinite(scale)) return VIT_ERR_ARG;
+    if (L == 0 && n_vision == 0) return VIT_OK;   // an empty prompt: nothing to read or write
+    if (!input_ids || !embed_table || !out || !embed_sizes_ok(L, vocab, dim) || n_vision < 0 || (n_vision > 0 && !vision))
+        return VIT_ERR_ARG;
+    if (!aligned16(embed_table) || !aligned16(out) || (vision && !aligned16(vision))) return VIT_ERR_ALIGN;
+    return vith::embed_launch(input_ids, L, embed_table, dtype, vocab, dim, scale, vision, n_vision, out, dev_status,
+                              static_cast<cudaStream_t>(stream));
+}
+
+int64_t embed_vision_tokens_grad_workspace(int64_t L, int64_t vocab, int dim) {
+    return embed_sizes_ok(L, vocab, dim) ? vith::embed_grad_workspace(L, vocab, dim) : 0;
+}
+
+int embed_vision_tokens_grad(const int32_t *input_ids, int64_t L, const void *d_out, int dtype, int64_t vocab, int dim,
+                             float scale, void *d_table, int table_dtype, int accumulate, void *d_vision,
+                             int64_t n_vision, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                             void *stream) {
+    if (!known_dtype(dtype) || (table_dtype != dtype && table_dtype != VIT_DTYPE_F32) || !std::isfinite(scale))
+        return VIT_ERR_ARG;
+    if (!embed_sizes_ok(L, vocab, dim) || n_vision < 0 || n_vision > (int64_t(1) << 30) || !d_table ||
+        (n_vision > 0 && !d_vision) || (L > 0 && (!input_ids || !d_out)))
+        return VIT_ERR_ARG;
+    if (!workspace || workspace_bytes < vith::embed_grad_workspace(L, vocab, dim)) return VIT_ERR_ARG;
+    if (!aligned16(d_table) || !aligned16(workspace) || (d_vision && !aligned16(d_vision)) || (d_out && !aligned16(d_out)))
+        return VIT_ERR_ALIGN;
+    return vith::embed_grad_launch(input_ids, L, d_out, dtype, vocab, dim, scale, d_table, table_dtype, accumulate != 0,
+                                   d_vision, n_vision, workspace, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int64_t prefix_attention_workspace(const prefix_attention_desc *desc) {
+    return check_prefix(desc) == VIT_OK ? vith::prefix_attention_bytes(*desc) : 0;
+}
+
+int prefix_attention(const prefix_attention_desc *desc, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
+                     void *stream) {
+    const int rc = check_prefix(desc);
+    if (rc != VIT_OK || desc->total_q == 0) return rc;
+    const int64_t need = vith::prefix_attention_bytes(*desc);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return VIT_ERR_ARG;
+    if (need > 0 && !aligned16(workspace)) return VIT_ERR_ALIGN;
+    return vith::prefix_attention_launch(*desc, workspace, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 int vit_op_wait_selftest(int32_t *dev_status, int64_t limit_cycles, void *stream) {

@@ -20,7 +20,9 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
+#include "dtype.cuh"
 #include "internal.h"
 
 namespace vitk {
@@ -109,11 +111,24 @@ __device__ __forceinline__ int is_vision(int id) {
     return (id == VIT_IMAGE_TOKEN_ID || id == VIT_VIDEO_TOKEN_ID) ? 1 : 0;
 }
 
+// v * scale element by element in fp32, rounded once
+template <typename T>
+__device__ __forceinline__ uint4 scale_vec(const uint4 &v, float scale) {
+    float f[Vec<T>::kVec];
+    Vec<T>::unpack(v, f);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::kVec; ++e) f[e] *= scale;
+    return Vec<T>::pack(f);
+}
+
+// T: element type of embedding rows that are scaled on the way (vision rows are copied); void: plain
+// copies of whole 16-byte vectors, whatever they hold
+template <typename T>
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const int32_t *__restrict__ ids, int64_t L,
                                                                   const uint4 *__restrict__ table, int64_t vocab,
                                                                   const uint4 *__restrict__ vision, int64_t n_vision,
                                                                   int row_vecs, uint4 *__restrict__ out,
-                                                                  int chunk, int32_t *status) {
+                                                                  int chunk, float scale, int32_t *status) {
     __shared__ int s_warp[kScatterThreads / 32];
     __shared__ int s_rank[kScatterMaxChunk];
     __shared__ int s_total;
@@ -167,7 +182,13 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const int32_t 
                 if (c + 32 * e < row_vecs) v[e] = __ldg(src + c + 32 * e);
 #pragma unroll
             for (int e = 0; e < kScatterUnroll; ++e)
-                if (c + 32 * e < row_vecs) dst[c + 32 * e] = v[e];
+                if (c + 32 * e < row_vecs) {
+                    if constexpr (std::is_same_v<T, void>) {
+                        dst[c + 32 * e] = v[e];
+                    } else {
+                        dst[c + 32 * e] = rank < 0 ? scale_vec<T>(v[e], scale) : v[e];
+                    }
+                }
         }
     }
 }
@@ -189,8 +210,11 @@ int mrope_apply_launch(void *q, int Hq, void *k, int Hk, int D, const int32_t *p
     return cudaGetLastError() == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
-int scatter_launch(const int32_t *ids, int64_t L, const void *table, int64_t vocab, int dim, const void *vision,
-                   int64_t n_vision, void *out, int32_t *status, cudaStream_t s) {
+namespace {
+
+template <typename T>
+int scatter_rows(const int32_t *ids, int64_t L, const void *table, int64_t vocab, int64_t row_bytes, const void *vision,
+                 int64_t n_vision, void *out, float scale, int32_t *status, cudaStream_t s) {
     if (L <= 0) return VIT_OK;
     // about 8 CTAs per SM: chunks of 8 tokens or more (a multiple of 8), so that at most ~1200
     // CTAs recount the prefix of the ids
@@ -198,10 +222,28 @@ int scatter_launch(const int32_t *ids, int64_t L, const void *table, int64_t voc
     chunk = chunk < 8 ? 8 : (chunk + 7) / 8 * 8;
     if (chunk > vitk::kScatterMaxChunk) return VIT_ERR_LIMIT;
     const int64_t chunks = (L + chunk - 1) / chunk;
-    vitk::scatter_kernel<<<static_cast<unsigned>(chunks), vitk::kScatterThreads, 0, s>>>(
-        ids, L, static_cast<const uint4 *>(table), vocab, static_cast<const uint4 *>(vision), n_vision, dim / 8,
-        static_cast<uint4 *>(out), static_cast<int>(chunk), status);
+    vitk::scatter_kernel<T><<<static_cast<unsigned>(chunks), vitk::kScatterThreads, 0, s>>>(
+        ids, L, static_cast<const uint4 *>(table), vocab, static_cast<const uint4 *>(vision), n_vision,
+        static_cast<int>(row_bytes / 16), static_cast<uint4 *>(out), static_cast<int>(chunk), scale, status);
     return cudaGetLastError() == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+}
+
+}  // namespace
+
+int scatter_launch(const int32_t *ids, int64_t L, const void *table, int64_t vocab, int dim, const void *vision,
+                   int64_t n_vision, void *out, int32_t *status, cudaStream_t s) {
+    return scatter_rows<void>(ids, L, table, vocab, int64_t(2) * dim, vision, n_vision, out, 1.0f, status, s);
+}
+
+int embed_launch(const int32_t *ids, int64_t L, const void *table, int dtype, int64_t vocab, int dim, float scale,
+                 const void *vision, int64_t n_vision, void *out, int32_t *status, cudaStream_t s) {
+    const int64_t row = (dtype == VIT_DTYPE_F32 ? int64_t(4) : int64_t(2)) * dim;
+    if (scale == 1.0f) return scatter_rows<void>(ids, L, table, vocab, row, vision, n_vision, out, scale, status, s);
+    if (dtype == VIT_DTYPE_BF16)
+        return scatter_rows<__nv_bfloat16>(ids, L, table, vocab, row, vision, n_vision, out, scale, status, s);
+    if (dtype == VIT_DTYPE_F16)
+        return scatter_rows<__half>(ids, L, table, vocab, row, vision, n_vision, out, scale, status, s);
+    return scatter_rows<float>(ids, L, table, vocab, row, vision, n_vision, out, scale, status, s);
 }
 
 }  // namespace vith

@@ -1,0 +1,510 @@
+// embed_grad.cu -- gradient of the decoder's input rows (embed_vision_tokens): the embedding table's
+// and the vision tokens'.
+//
+// Mathematics: d_table[v] = scale * sum over the text positions i with id v of d_out[i], and
+// d_vision[k] = d_out[slot of the k-th placeholder] ("Qwen2-VL (Native-Resolution VLM)", Structure
+// rows 6-10: merged image tokens and embedded text tokens form one sequence). The positions are
+// sorted by id first, so that every table row is summed once, in fp32, in ascending order of
+// position, whatever the scheduling: no floating-point atomics, the same bits on every run.
+//
+//   embed_sort_kernel    one cluster sorts (id, position) by a stable radix sort of 9-bit digits, one
+//                        contiguous share per CTA, one contiguous range per warp; placeholders and
+//                        ids outside the table get the keys vocab and vocab + 1 and end up behind the
+//                        text, so the k-th placeholder is entry n_text + k. The CTAs meet at the
+//                        cluster's hardware barrier, so nothing spins on memory.
+//   embed_reduce_kernel  sorted entries in chunks of a fixed size: a chunk's CTA adds up the rows of
+//                        each run of equal ids and writes the runs that lie inside the chunk; runs
+//                        that cross a border leave fp32 partial rows. Other CTAs of the same launch
+//                        copy the placeholders' rows and write zeros to the rows no token named (a
+//                        bit per table row, set by the sort).
+//   embed_join_kernel    adds the partial rows of each run that crosses chunks, in chunk order.
+//
+// Bound by HBM: d_out is read once and, unless accumulating, the whole table's gradient is written
+// once (152064 rows against a few thousand tokens: the zeros are most of the bytes).
+#include <algorithm>
+
+#include "dtype.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace vitk {
+
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortBits = 9, kSortBins = 1 << kSortBits;
+constexpr int kSortSmem = (kSortWarps + 1) * kSortBins * 4 + 64 * 4;
+constexpr int kSortOneCta = 4096;         // up to this many tokens one CTA sorts alone
+constexpr int kSortCluster = 8;
+
+struct EmbedWs {                          // device workspace of one call
+    uint2 *a, *b;                         // (key, position) buffers, L each
+    uint32_t *hist;                       // [cluster][kSortBins] of the current pass, twice (ping-pong)
+    int *count;                           // [cluster][2] text and vision tokens of each CTA's share
+    int *head;                            // n_text, n_vision found
+    uint32_t *named;                      // a bit per table row
+    float *part;                          // [2][chunks][dim] partial rows: heads, then tails
+};
+
+__device__ __forceinline__ uint32_t embed_key(int id, int64_t vocab) {
+    if (id == VIT_IMAGE_TOKEN_ID || id == VIT_VIDEO_TOKEN_ID) return static_cast<uint32_t>(vocab);
+    return id >= 0 && id < vocab ? static_cast<uint32_t>(id) : static_cast<uint32_t>(vocab) + 1u;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+    embed_sort_kernel(const int32_t *__restrict__ ids, int L, int64_t vocab, int64_t n_vision, int passes, int ctas,
+                      bool mark, EmbedWs ws, int32_t *status) {
+    extern __shared__ uint32_t s_hist[];                       // [warps][bins], then [bins]
+    uint32_t *s_base = s_hist + kSortWarps * kSortBins;
+    uint32_t *s_scan = s_base + kSortBins;                     // 32 warp sums
+    int *s_cnt = reinterpret_cast<int *>(s_scan + 32);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x;                               // one cluster: rank in it
+    const int per_warp = ((L + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+    const int w0 = min(L, (rank * kSortWarps + warp) * per_warp), w1 = min(L, w0 + per_warp);
+    uint32_t *hist = s_hist + warp * kSortBins;
+    if (tid < 2) s_cnt[tid] = 0;
+    if (mark)
+        for (int64_t i = static_cast<int64_t>(rank) * kSortThreads + tid; i < (vocab + 31) / 32; i += ctas * kSortThreads)
+            ws.named[i] = 0;
+    __syncthreads();
+    const uint2 *src = ws.b;
+    uint2 *dst = ws.a;
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * kSortBits;
+        auto entry = [&](int i) {
+            return p == 0 ? make_uint2(embed_key(ids[i], vocab), static_cast<uint32_t>(i))
+                          : __ldcg(src + i);
+        };
+        for (int d = lane; d < kSortBins; d += 32) hist[d] = 0;
+        __syncwarp();
+        int n_text = 0, n_vis = 0;
+        for (int i0 = w0; i0 < w1; i0 += 32) {                 // digits of this warp's range
+            const int i = i0 + lane;
+            const bool in = i < w1;
+            const uint32_t key = in ? entry(i).x : 0u;
+            const uint32_t d = in ? (key >> shift) & (kSortBins - 1) : kSortBins + lane;
+            if (p == 0) {
+                n_text += in && key < vocab;
+                n_vis += in && key == vocab;
+            }
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            if (in && (same & ((1u << lane) - 1u)) == 0) hist[d] += __popc(same);
+            __syncwarp();
+        }
+        if (p == 0) {
+            n_text = __reduce_add_sync(0xffffffffu, n_text);
+            n_vis = __reduce_add_sync(0xffffffffu, n_vis);
+            if (lane == 0) {
+                atomicAdd(s_cnt, n_text);
+                atomicAdd(s_cnt + 1, n_vis);
+            }
+        }
+        __syncthreads();
+        uint32_t *gh = ws.hist + (p & 1) * kSortCluster * kSortBins;
+        if (tid < kSortBins) {                                 // exclusive over the warps; the CTA's total
+            uint32_t run = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = s_hist[w * kSortBins + tid];
+                s_hist[w * kSortBins + tid] = run;
+                run += c;
+            }
+            gh[rank * kSortBins + tid] = run;
+        }
+        if (p == 0 && tid < 2) ws.count[rank * 2 + tid] = s_cnt[tid];
+        if (ctas > 1) {
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
+        if (tid < kSortBins) {                                 // first place of each digit for this CTA
+            uint32_t all = 0, before = 0;
+            for (int c = 0; c < ctas; ++c) {
+                const uint32_t h = __ldcg(gh + c * kSortBins + tid);
+                if (c < rank) before += h;
+                all += h;
+            }
+            uint32_t inc = all;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            if (lane == 31) s_scan[warp] = inc;
+            s_base[tid] = inc - all + before;
+        }
+        __syncthreads();
+        if (tid < kSortBins) {
+            uint32_t add = 0;
+            for (int w = 0; w < warp; ++w) add += s_scan[w];
+            s_base[tid] += add;
+        }
+        __syncthreads();
+        for (int d = lane; d < kSortBins; d += 32) hist[d] += s_base[d];
+        __syncwarp();
+        for (int i0 = w0; i0 < w1; i0 += 32) {                 // stable: ranks inside a warp by lane
+            const int i = i0 + lane;
+            const bool in = i < w1;
+            const uint2 e = in ? entry(i) : make_uint2(0u, 0u);
+            const uint32_t d = in ? (e.x >> shift) & (kSortBins - 1) : kSortBins + lane;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            const uint32_t at = in ? hist[d] + __popc(same & ((1u << lane) - 1u)) : 0u;
+            __syncwarp();
+            if (in) {
+                dst[at] = e;
+                if ((same >> lane) == 1u) hist[d] = at + 1u;   // the last lane of each digit
+                if (p == 0 && mark && e.x < vocab) atomicOr(ws.named + (e.x >> 5), 1u << (e.x & 31));
+            }
+            __syncwarp();
+        }
+        if (p == 0 && rank == 0 && tid == 0) {
+            int t = 0, v = 0;
+            for (int c = 0; c < ctas; ++c) {
+                t += __ldcg(ws.count + 2 * c);
+                v += __ldcg(ws.count + 2 * c + 1);
+            }
+            ws.head[0] = t;
+            ws.head[1] = v;
+            if (status && (v != n_vision || t + v != L)) atomicExch(status, VIT_ERR_TOKENS);
+        }
+        if (ctas > 1) {
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
+        src = dst;
+        dst = dst == ws.a ? ws.b : ws.a;
+    }
+}
+
+constexpr int kReduceThreads = 128, kSlab = 8 * kReduceThreads;   // columns per CTA
+constexpr int kMaxChunk = 256;
+constexpr int kZeroRows = 32;                                     // table rows per zero-writing CTA
+
+template <typename G>
+__device__ __forceinline__ void store8(G *p, const float *v) {
+    *reinterpret_cast<uint4 *>(p) = Vec<G>::pack(v);
+}
+template <>
+__device__ __forceinline__ void store8<float>(float *p, const float *v) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <typename T>
+struct Row8 {                                                     // 8 consecutive elements as loaded
+    uint4 v;
+    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float *f) const { Vec<T>::unpack(v, f); }
+};
+template <>
+struct Row8<float> {
+    uint4 v, w;
+    __device__ __forceinline__ void load(const float *p) {
+        v = reinterpret_cast<const uint4 *>(p)[0];
+        w = reinterpret_cast<const uint4 *>(p)[1];
+    }
+    __device__ __forceinline__ void get(float *f) const {
+        Vec<float>::unpack(v, f);
+        Vec<float>::unpack(w, f + 4);
+    }
+};
+
+// d_table[row][col..col+8) = (old +) scale * sum, rounded once
+template <typename G>
+__device__ __forceinline__ void write_row8(G *d_table, int64_t row, int dim, int col, const float *sum, float scale,
+                                           bool accumulate) {
+    G *p = d_table + row * dim + col;
+    float o[8];
+    if (accumulate) {
+        Row8<G> old;
+        old.load(p);
+        old.get(o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += sum[e] * scale;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = sum[e] * scale;
+    }
+    store8<G>(p, o);
+}
+
+struct EmbedReduceArgs {
+    const uint2 *sorted;
+    const int *head;
+    const uint32_t *named;
+    float *part;
+    const void *d_out;
+    void *d_table;
+    void *d_vision;
+    int64_t vocab, n_vision;
+    int dim, chunk, n_chunks, slabs;
+    int sum_ctas, vision_ctas;
+    float scale;
+    bool accumulate;
+};
+
+template <typename T, typename G>
+__global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const __grid_constant__ EmbedReduceArgs a) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_text = a.head[0];
+    if (blockIdx.x < a.sum_ctas) {                            // ---- a chunk's runs
+        __shared__ uint32_t s_key[kMaxChunk + 2];             // entries c0 - 1 .. c0 + n
+        __shared__ uint32_t s_pos[kMaxChunk];
+        const int chunk = blockIdx.x / a.slabs, col = (blockIdx.x % a.slabs) * kSlab + tid * 8;
+        const int c0 = chunk * a.chunk;
+        const int n = min(a.chunk, n_text - c0);
+        if (n <= 0) return;
+        constexpr uint32_t kNone = 0xffffffffu;
+        for (int i = tid; i < n + 2; i += kReduceThreads) {
+            const int at = c0 - 1 + i;
+            const bool in = at >= 0 && at < n_text;
+            const uint2 e = in ? a.sorted[at] : make_uint2(kNone, 0u);
+            s_key[i] = e.x;
+            if (i >= 1 && i <= n) s_pos[i - 1] = e.y;
+        }
+        __syncthreads();
+        if (col >= a.dim) return;
+        const T *d_out = static_cast<const T *>(a.d_out) + col;
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        bool from_before = s_key[0] == s_key[1];              // the first run started in an earlier chunk
+        constexpr int kAhead = 8;
+        for (int e0 = 0; e0 < n; e0 += kAhead) {
+            Row8<T> r[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (e0 + u < n) r[u].load(d_out + static_cast<int64_t>(s_pos[e0 + u]) * a.dim);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int e = e0 + u;
+                if (e >= n) break;
+                float f[8];
+                r[u].get(f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += f[i];
+                const bool more = s_key[e + 2] == s_key[e + 1];
+                if (more && e + 1 < n) continue;
+                if (from_before) {
+                    store8<float>(a.part + static_cast<int64_t>(chunk) * a.dim + col, acc);
+                } else if (more) {
+                    store8<float>(a.part + static_cast<int64_t>(a.n_chunks + chunk) * a.dim + col, acc);
+                } else {
+                    write_row8<G>(static_cast<G *>(a.d_table), s_key[e + 1], a.dim, col, acc, a.scale, a.accumulate);
+                }
+                from_before = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+            }
+        }
+    } else if (blockIdx.x < a.sum_ctas + a.vision_ctas) {     // ---- placeholders' rows, one per warp
+        const int64_t k = static_cast<int64_t>(blockIdx.x - a.sum_ctas) * (kReduceThreads / 32) + warp;
+        if (k >= a.n_vision) return;
+        const int vecs = a.dim * static_cast<int>(sizeof(T)) / 16;
+        uint4 *dst = static_cast<uint4 *>(a.d_vision) + k * vecs;
+        const bool found = k < a.head[1];                     // fewer placeholders than vision tokens: zeros
+        const uint4 *src = static_cast<const uint4 *>(a.d_out) +
+                           (found ? static_cast<int64_t>(a.sorted[n_text + k].y) * vecs : 0);
+        for (int c = lane; c < vecs; c += 32 * 8) {
+            uint4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (found && c + 32 * u < vecs) v[u] = __ldg(src + c + 32 * u);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + 32 * u < vecs) dst[c + 32 * u] = v[u];
+        }
+    } else {                                                  // ---- rows no token named: zeros
+        const int64_t r0 = static_cast<int64_t>(blockIdx.x - a.sum_ctas - a.vision_ctas) * kZeroRows;
+        const uint32_t bits = a.named[r0 / 32];
+        const int vecs = a.dim * static_cast<int>(sizeof(G)) / 16;
+        for (int i = warp; i < kZeroRows && r0 + i < a.vocab; i += kReduceThreads / 32) {
+            if ((bits >> i) & 1u) continue;
+            uint4 *dst = static_cast<uint4 *>(a.d_table) + (r0 + i) * vecs;
+            for (int c = lane; c < vecs; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+static_assert(kZeroRows == 32, "one word of row bits per zero-writing CTA");
+
+constexpr int kJoinThreads = 256, kJoinCols = 256, kJoinGroups = kJoinThreads / (kJoinCols / 4);
+
+template <typename G>
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_constant__ EmbedReduceArgs a) {
+    const int n_text = a.head[0];
+    const int chunk = blockIdx.x, c0 = chunk * a.chunk, c1 = c0 + a.chunk;
+    if (c1 >= n_text) return;                                 // the last chunk ends its runs
+    const uint32_t key = a.sorted[c1 - 1].x;
+    if (a.sorted[c1].x != key) return;                        // no run leaves this chunk
+    if (c0 > 0 && a.sorted[c0 - 1].x == key) return;          // the run started in an earlier chunk
+    int lo = c1, hi = n_text;                                 // first entry behind the run
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.sorted[mid].x == key) {
+            lo = mid + 1;
+        } else {
+            hi = mid;
+        }
+    }
+    const int last = (lo - 1) / a.chunk;                      // the chunk in which the run ends
+    __shared__ float4 s[kJoinGroups][kJoinCols / 4];
+    const int tc = threadIdx.x % (kJoinCols / 4), grp = threadIdx.x / (kJoinCols / 4);
+    const int col = blockIdx.y * kJoinCols + tc * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < a.dim) {
+        // partial 0 is the run's tail in its first chunk, partial i the head of chunk + i
+#pragma unroll 4
+        for (int i = grp; i <= last - chunk; i += kJoinGroups) {
+            const int64_t row = i == 0 ? a.n_chunks + chunk : chunk + i;
+            const float4 v = *reinterpret_cast<const float4 *>(a.part + row * a.dim + col);
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+    }
+    s[grp][tc] = acc;
+    __syncthreads();
+    if (threadIdx.x < kJoinCols / 8) {
+        const int c8 = blockIdx.y * kJoinCols + threadIdx.x * 8;
+        if (c8 < a.dim) {
+            float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int gi = 0; gi < kJoinGroups; ++gi) {
+                const float4 u = s[gi][2 * threadIdx.x], v = s[gi][2 * threadIdx.x + 1];
+                t[0] += u.x;
+                t[1] += u.y;
+                t[2] += u.z;
+                t[3] += u.w;
+                t[4] += v.x;
+                t[5] += v.y;
+                t[6] += v.z;
+                t[7] += v.w;
+            }
+            write_row8<G>(static_cast<G *>(a.d_table), key, a.dim, c8, t, a.scale, a.accumulate);
+        }
+    }
+}
+
+}  // namespace vitk
+
+namespace vith {
+
+namespace {
+
+// Sorted entries per chunk: about eight CTAs per SM over all column slabs, 8 .. kMaxChunk entries.
+// Small chunks give short prompts enough CTAs; large ones keep the partial rows few.
+int chunk_size(int64_t L, int slabs) {
+    int c = 8;
+    while (c < vitk::kMaxChunk && c * int64_t(148 * 8) < L * slabs) c *= 2;
+    return c;
+}
+
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+// Lays the workspace out at `base` (which may be null to learn the size only).
+size_t layout(char *base, int64_t L, int64_t vocab, int dim, vitk::EmbedWs *w) {
+    const int slabs = (dim + vitk::kSlab - 1) / vitk::kSlab, chunk = chunk_size(L, slabs);
+    const int64_t chunks = (L + chunk - 1) / chunk;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char *p = base + at;
+        at += up16(bytes);
+        return p;
+    };
+    vitk::EmbedWs ws;
+    ws.a = reinterpret_cast<uint2 *>(take(L * sizeof(uint2)));
+    ws.b = reinterpret_cast<uint2 *>(take(L * sizeof(uint2)));
+    ws.hist = reinterpret_cast<uint32_t *>(take(2 * vitk::kSortCluster * vitk::kSortBins * 4));
+    ws.count = reinterpret_cast<int *>(take(vitk::kSortCluster * 2 * 4));
+    ws.head = reinterpret_cast<int *>(take(2 * 4));
+    ws.named = reinterpret_cast<uint32_t *>(take((vocab + 31) / 32 * 4));
+    ws.part = reinterpret_cast<float *>(take(2 * chunks * dim * sizeof(float)));
+    if (w) *w = ws;
+    return at;
+}
+
+bool configure_sort() {
+    static bool configured[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && configured[dev]) return true;
+    if (cudaFuncSetAttribute(vitk::embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, vitk::kSortSmem) !=
+        cudaSuccess)
+        return false;
+    if (dev < 64) configured[dev] = true;
+    return true;
+}
+
+template <typename T, typename G>
+cudaError_t reduce(const vitk::EmbedReduceArgs &a, cudaStream_t s) {
+    const int64_t zero = a.accumulate ? 0 : (a.vocab + vitk::kZeroRows - 1) / vitk::kZeroRows;
+    const int64_t grid = a.sum_ctas + a.vision_ctas + zero;
+    if (grid > 0)
+        vitk::embed_reduce_kernel<T, G><<<static_cast<unsigned>(grid), vitk::kReduceThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && a.n_chunks > 1) {
+        vitk::embed_join_kernel<G><<<dim3(a.n_chunks - 1, (a.dim + vitk::kJoinCols - 1) / vitk::kJoinCols),
+                                     vitk::kJoinThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+int64_t embed_grad_workspace(int64_t L, int64_t vocab, int dim) {
+    return static_cast<int64_t>(layout(nullptr, L, vocab, dim, nullptr));
+}
+
+int embed_grad_launch(const int32_t *ids, int64_t L, const void *d_out, int dtype, int64_t vocab, int dim, float scale,
+                      void *d_table, int table_dtype, bool accumulate, void *d_vision, int64_t n_vision, void *workspace,
+                      int32_t *status, cudaStream_t s) {
+    if (!configure_sort()) return VIT_ERR_CUDA;
+    vitk::EmbedWs ws;
+    layout(static_cast<char *>(workspace), L, vocab, dim, &ws);
+    int bits = 1;
+    while (bits < 32 && (int64_t(1) << bits) < vocab + 2) ++bits;
+    const int passes = (bits + vitk::kSortBits - 1) / vitk::kSortBits;
+    const int ctas = L <= vitk::kSortOneCta ? 1 : vitk::kSortCluster;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(vitk::kSortThreads);
+    cfg.dynamicSmemBytes = vitk::kSortSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, vitk::embed_sort_kernel, ids, static_cast<int>(L), vocab, n_vision, passes, ctas,
+                           !accumulate, ws, status) != cudaSuccess)
+        return VIT_ERR_CUDA;
+    vitk::EmbedReduceArgs a;
+    a.sorted = passes % 2 ? ws.a : ws.b;
+    a.head = ws.head;
+    a.named = ws.named;
+    a.part = ws.part;
+    a.d_out = d_out;
+    a.d_table = d_table;
+    a.d_vision = d_vision;
+    a.vocab = vocab;
+    a.n_vision = n_vision;
+    a.dim = dim;
+    a.slabs = (dim + vitk::kSlab - 1) / vitk::kSlab;
+    a.chunk = chunk_size(L, a.slabs);
+    a.n_chunks = static_cast<int>((L + a.chunk - 1) / a.chunk);
+    a.sum_ctas = a.n_chunks * a.slabs;
+    a.vision_ctas = static_cast<int>((n_vision + vitk::kReduceThreads / 32 - 1) / (vitk::kReduceThreads / 32));
+    a.scale = scale;
+    a.accumulate = accumulate;
+    cudaError_t e;
+    if (dtype == VIT_DTYPE_F32)
+        e = reduce<float, float>(a, s);
+    else if (dtype == VIT_DTYPE_BF16)
+        e = table_dtype == VIT_DTYPE_F32 ? reduce<__nv_bfloat16, float>(a, s) : reduce<__nv_bfloat16, __nv_bfloat16>(a, s);
+    else
+        e = table_dtype == VIT_DTYPE_F32 ? reduce<__half, float>(a, s) : reduce<__half, __half>(a, s);
+    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+}
+
+}  // namespace vith

@@ -109,6 +109,35 @@ int mrope_apply_launch(void *q, int Hq, void *k, int Hk, int D, const int32_t *p
                        const int32_t *sections, cudaStream_t s);
 int scatter_launch(const int32_t *ids, int64_t L, const void *table, int64_t vocab, int dim, const void *vision,
                    int64_t n_vision, void *out, int32_t *status, cudaStream_t s);
+// embed_vision_tokens: the scatter with embedding rows scaled on the way
+int embed_launch(const int32_t *ids, int64_t L, const void *table, int dtype, int64_t vocab, int dim, float scale,
+                 const void *vision, int64_t n_vision, void *out, int32_t *status, cudaStream_t s);
+// its gradient (embed_grad.cu)
+int64_t embed_grad_workspace(int64_t L, int64_t vocab, int dim);
+int embed_grad_launch(const int32_t *ids, int64_t L, const void *d_out, int dtype, int64_t vocab, int dim, float scale,
+                      void *d_table, int table_dtype, bool accumulate, void *d_vision, int64_t n_vision, void *workspace,
+                      int32_t *status, cudaStream_t s);
+// ---- per-head norm and M-RoPE of q and k (norm_rope.cu); index 0 is q, 1 is k, strides in elements
+struct NormRopeCall {
+    const void *x[2];
+    void *y[2];            // outputs; dq, dk in the gradient
+    const void *dy[2];     // gradient only
+    const void *w[2];
+    int64_t x_stride[2], y_stride[2], dy_stride[2];
+    int heads[2];
+    int head_dim, dtype;
+    float eps;
+    const int32_t *pos;
+    int64_t L;
+    double theta;
+    const int32_t *sections;   // HOST [3]
+};
+int norm_rope_launch(const NormRopeCall &c, cudaStream_t s);
+int64_t norm_rope_grad_workspace(int head_dim);
+int norm_rope_grad_launch(const NormRopeCall &c, float *dqw, float *dkw, void *workspace, cudaStream_t s);
+// ---- attention over a shared prefix (prefix_attn.cu)
+int64_t prefix_attention_bytes(const prefix_attention_desc &d);
+int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int32_t *status, cudaStream_t s);
 int wait_selftest_launch(int32_t *status, long long limit, cudaStream_t s);
 int mrope_launch(const int32_t *ids, int64_t L, const int32_t *grid_thw, int n_grids, int32_t *out, int32_t *delta,
                  int32_t *status, cudaStream_t s);

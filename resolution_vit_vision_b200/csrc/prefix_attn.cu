@@ -1,0 +1,473 @@
+// prefix_attn.cu -- attention of a batch of sequences over a prefix they all share and over each
+// one's own keys: few query rows per sequence (decoding) and the join of partial results.
+//
+// Mathematics, for a query row i (token, head): o = sum_s p_s v_s / sum_s p_s, p_s = exp(scale q k_s
+// - m), m the running maximum, over the prefix keys and the row's visible own keys. The keys may be
+// cut into parts in any way: a part gives o and lse = log sum exp, and parts join as
+// o = sum_j w_j o_j / sum_j w_j, w_j = exp(lse_j - max lse). Hence the prefix part can be computed for
+// the stacked queries of the whole batch, its K and V read once for all of them.
+//
+//   prefix_small_kernel   row tiles of 16 or 64 query rows (a row is a token and one of the G query
+//                         heads of a key-value head, so G x tokens rows share every key), keys in
+//                         tiles of 64 through a 3-deep cp.async ring, m16n8k16 tensor-core products
+//                         with fp32 sums; with 16 rows the four warps take a quarter of each key tile
+//                         and join at the end. Rows of few queries are bound by reading K and V from
+//                         HBM: the products of a 16-row tile need about a fifth of the time its keys
+//                         take to arrive, so the wider tensor-core path would idle.
+//   prefix_join_kernel    one warp per (token, head): joins the parts.
+// Statistics and sums are fp32; P is rounded to the element type for the P V product (weights at most
+// 1: the error of o is half an element step of max |v|), o is rounded once at the end.
+#include <algorithm>
+
+#include "dtype.cuh"
+#include "internal.h"
+#include "prefix_attn.h"
+#include "ptx.cuh"
+
+namespace vitk {
+
+constexpr int kSmThreads = 128, kSmKeys = 64, kSmStages = 3;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         __nv_bfloat16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_mufu(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Shared bytes of a key (or value) row: 16 more than the head, an odd number of 16-byte words, so the
+// eight rows of an ldmatrix fall into different banks.
+template <int DP>
+constexpr int kSmRow = DP * 2 + 16;
+template <int DP>
+constexpr int kSmTileBytes = kSmKeys * kSmRow<DP>;
+template <int DP>
+constexpr int kSmSmem = kSmStages * 2 * kSmTileBytes<DP>;
+
+// kind 0: items over the stacked queries and the prefix; 1: a sequence's items over its own keys
+// (stacked plan) or over prefix and own keys (the other plan)
+template <typename T, int DP, int WR, int WK>
+__global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __grid_constant__ PrefixArgs a, int kind) {
+    static_assert(WR * WK == kSmThreads / 32, "four warps");
+    constexpr int M = 16 * WR, KW = kSmKeys / WK, NT = KW / 8, DT = DP / 8, KS = DP / 16;
+    constexpr int kRow = kSmRow<DP>;
+    extern __shared__ uint4 sm_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>(sm_raw);
+    const prefix_attention_desc &d = a.d;
+    const PrefixPlan &pl = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp / WK, wk = warp % WK;
+    const int D = d.head_dim, G = pl.G;
+
+    // ---- the item: rows [row0, row0 + rows) of a run of queries, key tiles [t0, t1) of its list
+    const int h = blockIdx.x % d.n_kv_heads;
+    int rest = blockIdx.x / d.n_kv_heads;
+    int64_t q0;                                   // first token of the run
+    int n_q, len = 0, b = 0, part;
+    int row0, t0, t1, n_prefix_tiles, own_keys = 0;
+    const int prefix_tiles = static_cast<int>((d.prefix_len + kSmKeys - 1) / kSmKeys);
+    if (kind == 0) {
+        part = rest % pl.prefix_splits;
+        row0 = rest / pl.prefix_splits * M;
+        q0 = 0;
+        n_q = static_cast<int>(d.total_q);
+        n_prefix_tiles = prefix_tiles;
+        t0 = part * pl.prefix_tiles_per_split;
+        t1 = min(prefix_tiles, t0 + pl.prefix_tiles_per_split);
+    } else {
+        const int sp = rest % pl.seq_splits;
+        rest /= pl.seq_splits;
+        const int row_tiles = static_cast<int>((d.max_q * G + M - 1) / M);
+        row0 = rest % row_tiles * M;
+        b = rest / row_tiles;
+        const SeqRange r = seq_range(d, b);
+        if (!r.ok && tid == 0 && a.status) atomicExch(a.status, VIT_ERR_LIMIT);
+        q0 = r.q0;
+        n_q = r.n_q;
+        len = r.len;
+        if (row0 >= n_q * G) return;
+        n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
+        part = pl.prefix_splits + sp;
+        // keys behind the last row's own position are seen by no row of this tile
+        own_keys = len;
+        if (d.causal) own_keys = max(0, min(len, len - n_q + min(n_q - 1, (row0 + M - 1) / G) + 1));
+        const int total = n_prefix_tiles + (own_keys + kSmKeys - 1) / kSmKeys;
+        const int per = max(pl.min_tiles, (total + pl.seq_splits - 1) / pl.seq_splits);
+        t0 = min(total, sp * per);
+        t1 = min(total, t0 + per);
+    }
+    const int rows = min(M, n_q * G - row0);
+    auto token_of = [&](int r) { return q0 + (row0 + r) / G; };
+    auto head_of = [&](int r) { return h * G + (row0 + r) % G; };
+
+    auto load_tile = [&](int t, int stage) {
+        const bool pre = t < n_prefix_tiles;
+        const int k0 = (pre ? t : t - n_prefix_tiles) * kSmKeys;
+        const int n = static_cast<int>(min(static_cast<int64_t>(kSmKeys), (pre ? d.prefix_len : own_keys) - k0));
+        const T *kp = pre ? static_cast<const T *>(d.prefix_k) + h * d.prefix_k_head + k0 * d.prefix_k_token
+                          : static_cast<const T *>(d.k) + b * d.k_seq + h * d.k_head + k0 * d.k_token;
+        const T *vp = pre ? static_cast<const T *>(d.prefix_v) + h * d.prefix_v_head + k0 * d.prefix_v_token
+                          : static_cast<const T *>(d.v) + b * d.v_seq + h * d.v_head + k0 * d.v_token;
+        const int64_t ks = pre ? d.prefix_k_token : d.k_token, vs = pre ? d.prefix_v_token : d.v_token;
+        const uint32_t sk = smem_u32(sm) + stage * 2 * kSmTileBytes<DP>, sv = sk + kSmTileBytes<DP>;
+        // rows behind the last key and dims behind the head are zeros
+#pragma unroll 4
+        for (int i = tid; i < kSmKeys * (DP / 8); i += kSmThreads) {
+            const int r = i / (DP / 8), c = i % (DP / 8);
+            const bool in = r < n && c * 8 < D;
+            cp16(sk + r * kRow + c * 16, in ? kp + r * ks + c * 8 : kp, in);
+            cp16(sv + r * kRow + c * 16, in ? vp + r * vs + c * 8 : vp, in);
+        }
+    };
+
+    // ---- Q: through the last stage's buffer (not loaded before the loop starts) into registers
+    uint8_t *sq = sm + (kSmStages - 1) * 2 * kSmTileBytes<DP>;
+    for (int i = tid; i < M * (DP / 8); i += kSmThreads) {
+        const int r = i / (DP / 8), c = i % (DP / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows && c * 8 < D)
+            v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(d.q) + token_of(r) * d.q_stride +
+                                                 head_of(r) * D + c * 8);
+        *reinterpret_cast<uint4 *>(sq + r * kRow + c * 16) = v;
+    }
+#pragma unroll
+    for (int s = 0; s < kSmStages - 1; ++s) {
+        if (t0 + s < t1) load_tile(t0 + s, s);
+        cp_commit();
+    }
+    __syncthreads();
+    uint32_t qf[KS][4];
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+        ldsm4(qf[k], smem_u32(sq) + (wr * 16 + (lane & 15)) * kRow + (2 * k + (lane >> 4)) * 16);
+
+    float o[DT][4];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const float scale_log2 = d.scale * kLog2e;
+    // this thread's two rows: their last visible own key + 1
+    int lim[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = (row0 + wr * 16 + (lane >> 2) + 8 * i) / G;
+        lim[i] = kind == 0 ? 0 : (d.causal ? min(len, len - n_q + j + 1) : len);
+    }
+
+    for (int t = t0; t < t1; ++t) {
+        cp_wait<kSmStages - 2>();
+        __syncthreads();
+        const int nt = t + kSmStages - 1;
+        if (nt < t1) load_tile(nt, (nt - t0) % kSmStages);
+        cp_commit();
+        const uint32_t sk = smem_u32(sm) + (t - t0) % kSmStages * 2 * kSmTileBytes<DP> + wk * KW * kRow;
+        const uint32_t sv = sk + kSmTileBytes<DP>;
+        float s[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < NT; i += 2) {
+                uint32_t kf[4];
+                ldsm4(kf, sk + (i * 8 + (lane & 7) + ((lane >> 4) << 3)) * kRow + (2 * k + ((lane >> 3) & 1)) * 16);
+                mma16816(s[i], qf[k], kf[0], kf[1], T());
+                mma16816(s[i + 1], qf[k], kf[2], kf[3], T());
+            }
+        const bool pre = t < n_prefix_tiles;
+        const int k0 = (pre ? t : t - n_prefix_tiles) * kSmKeys + wk * KW;
+        const int lim0 = pre ? static_cast<int>(d.prefix_len) : lim[0], lim1 = pre ? static_cast<int>(d.prefix_len) : lim[1];
+        if (__any_sync(0xffffffffu, k0 + KW > min(lim0, lim1))) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (k0 + i * 8 + (lane & 3) * 2 + (e & 1) >= (e < 2 ? lim0 : lim1)) s[i][e] = -INFINITY;
+        }
+        float neg[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mx = fmaxf(mx, fmaxf(s[i][2 * r], s[i][2 * r + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scale_log2;
+            const float mn = fmaxf(m[r], mx);
+            const float off = mn == -INFINITY ? 0.f : mn;       // no visible key yet: every p stays 0
+            const float alpha = exp2_mufu(m[r] - off);
+            m[r] = mn;
+            l[r] *= alpha;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+                o[i][2 * r] *= alpha;
+                o[i][2 * r + 1] *= alpha;
+            }
+            neg[r] = -off;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[i][e] = exp2_mufu(fmaf(s[i][e], scale_log2, neg[e >> 1]));
+                l[e >> 1] += s[i][e];
+            }
+#pragma unroll
+        for (int k = 0; k < KW / 16; ++k) {
+            const uint32_t pf[4] = {pack2(s[2 * k][0], s[2 * k][1], T()), pack2(s[2 * k][2], s[2 * k][3], T()),
+                                    pack2(s[2 * k + 1][0], s[2 * k + 1][1], T()),
+                                    pack2(s[2 * k + 1][2], s[2 * k + 1][3], T())};
+#pragma unroll
+            for (int i = 0; i < DT; i += 2) {
+                uint32_t vf[4];
+                ldsm4t(vf, sv + (k * 16 + (lane & 15)) * kRow + (i + (lane >> 4)) * 16);
+                mma16816(o[i], pf, vf[0], vf[1], T());
+                mma16816(o[i + 1], pf, vf[2], vf[3], T());
+            }
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // ---- epilogue: the key groups' o, m, l through shared memory, joined, written
+    constexpr int kOP = DP + 4;                                // fp32 row pitch
+    float *so = reinterpret_cast<float *>(sm);                 // [WK][M][kOP]
+    float *sml = so + WK * M * kOP;                            // [WK][M][2]
+    static_assert((WK * M * kOP + 2 * WK * M) * 4 <= kSmSmem<DP>, "epilogue fits in the ring");
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        const int row = wr * 16 + (lane >> 2) + 8 * r;
+        if ((lane & 3) == 0) {
+            sml[(wk * M + row) * 2] = m[r];
+            sml[(wk * M + row) * 2 + 1] = l[r];
+        }
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+            *reinterpret_cast<float2 *>(so + (wk * M + row) * kOP + i * 8 + (lane & 3) * 2) =
+                make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    }
+    __syncthreads();
+    int64_t q_end = q0 + n_q;
+    if (kind == 0 && d.cu_q != nullptr) q_end = d.cu_q[d.n_seq];   // rows behind the last sequence stay as they were
+    for (int i = tid; i < rows * (DP / 8); i += kSmThreads) {
+        const int r = i / (DP / 8), c = i % (DP / 8) * 8;
+        if (c >= D) continue;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) mm = fmaxf(mm, sml[(w * M + r) * 2]);
+        const float off = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            const float f = exp2_mufu(sml[(w * M + r) * 2] - off);
+            ll += sml[(w * M + r) * 2 + 1] * f;
+            const float *p = so + (w * M + r) * kOP + c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += p[e] * f;
+        }
+        const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= inv;
+        const float lse2 = off + log2f(ll);                   // -inf where no key was visible
+        const int64_t token = token_of(r);
+        const int head = head_of(r);
+        if (pl.parts == 1) {
+            if (token >= q_end) continue;
+            *reinterpret_cast<uint4 *>(static_cast<T *>(d.out) + token * d.out_stride + head * D + c) = Vec<T>::pack(v);
+            if (c == 0 && d.lse) d.lse[token * d.n_heads + head] = lse2 * kLn2;
+        } else {
+            const int64_t row = (static_cast<int64_t>(part) * d.total_q + token) * d.n_heads + head;
+            float4 *p = reinterpret_cast<float4 *>(pl.part_o + row * D + c);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (c == 0) pl.part_lse[row] = lse2;
+        }
+    }
+}
+
+// One warp per (sequence, query, head): weights from the parts' lse, o joined in fp32, four dims per lane
+template <typename T>
+__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+    const prefix_attention_desc &d = a.d;
+    const PrefixPlan &pl = a.p;
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (w >= static_cast<int64_t>(d.n_seq) * d.max_q * d.n_heads) return;
+    const int head = static_cast<int>(w % d.n_heads);
+    const int64_t t = w / d.n_heads;
+    const int b = static_cast<int>(t / d.max_q), j = static_cast<int>(t % d.max_q);
+    const SeqRange r = seq_range(d, b);
+    if (j >= r.n_q) return;
+    const int64_t token = r.q0 + j;
+    const int64_t row = token * d.n_heads + head, pitch = d.total_q * d.n_heads;
+    float mx = -INFINITY;
+    for (int i = lane; i < pl.parts; i += 32) mx = fmaxf(mx, pl.part_lse[i * pitch + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float off = mx == -INFINITY ? 0.f : mx;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pl.parts; ++i) {
+        const float wt = exp2f(pl.part_lse[i * pitch + row] - off);
+        sum += wt;
+        if (wt != 0.f && lane * 4 < d.head_dim) {      // a part without keys was not written
+            const float4 v = *reinterpret_cast<const float4 *>(pl.part_o + (i * pitch + row) * d.head_dim + lane * 4);
+            acc.x += wt * v.x;
+            acc.y += wt * v.y;
+            acc.z += wt * v.z;
+            acc.w += wt * v.w;
+        }
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+    if (lane * 4 < d.head_dim)
+        *reinterpret_cast<uint2 *>(static_cast<T *>(d.out) + token * d.out_stride + head * d.head_dim + lane * 4) =
+            make_uint2(pack2(acc.x * inv, acc.y * inv, T()), pack2(acc.z * inv, acc.w * inv, T()));
+    if (lane == 0 && d.lse) d.lse[row] = (off + log2f(sum)) * kLn2;
+}
+
+}  // namespace vitk
+
+namespace vith {
+
+namespace {
+
+constexpr int kWaveItems = 148 * 2;       // CTAs resident at a time
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+template <typename T, int DP, int WR, int WK>
+cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s) {
+    if (items <= 0) return cudaSuccess;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(vitk::prefix_small_kernel<T, DP, WR, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 vitk::kSmSmem<DP>);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    vitk::prefix_small_kernel<T, DP, WR, WK>
+        <<<static_cast<unsigned>(items), vitk::kSmThreads, vitk::kSmSmem<DP>, s>>>(a, kind);
+    return cudaGetLastError();
+}
+
+template <typename T, int DP>
+cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, cudaStream_t s) {
+    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, s) : launch_small<T, DP, 4, 1>(a, kind, items, s);
+}
+
+template <typename T>
+cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, cudaStream_t s) {
+    if (a.d.head_dim <= 64) return small<T, 64>(a, kind, m, items, s);
+    if (a.d.head_dim <= 80) return small<T, 80>(a, kind, m, items, s);
+    return small<T, 128>(a, kind, m, items, s);
+}
+
+struct Plan {
+    vitk::PrefixPlan p;
+    int m_prefix, m_seq;                  // row tiles of the two kinds of items
+    int64_t prefix_items, seq_items;
+    size_t o_bytes, lse_bytes;
+};
+
+Plan make_plan(const prefix_attention_desc &d) {
+    Plan pn{};
+    vitk::PrefixPlan &p = pn.p;
+    p.G = d.n_heads / d.n_kv_heads;
+    const bool own = d.k != nullptr && d.max_len > 0;
+    const int prefix_tiles = ceil_div(d.prefix_len, vitk::kSmKeys), own_tiles = own ? ceil_div(d.max_len, vitk::kSmKeys) : 0;
+    pn.m_seq = d.max_q * p.G <= 16 ? 16 : 64;
+    pn.m_prefix = d.total_q * p.G <= 16 ? 16 : 64;
+    p.stacked = d.n_seq > 1 && prefix_tiles > 0 && d.total_q * p.G < int64_t(d.n_seq) * 64;
+    p.min_tiles = 4;
+    const int64_t seq_rows = int64_t(d.n_seq) * d.n_kv_heads * ceil_div(d.max_q * p.G, pn.m_seq);
+    if (p.stacked) {
+        const int64_t rows = int64_t(d.n_kv_heads) * ceil_div(d.total_q * p.G, pn.m_prefix);
+        int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kWaveItems / rows, prefix_tiles / p.min_tiles));
+        p.prefix_tiles_per_split = ceil_div(prefix_tiles, splits);
+        p.prefix_splits = ceil_div(prefix_tiles, p.prefix_tiles_per_split);
+        pn.prefix_items = rows * p.prefix_splits;
+    }
+    const int tiles = own_tiles + (p.stacked ? 0 : prefix_tiles);
+    if (!p.stacked || own) {
+        p.seq_splits = static_cast<int>(
+            std::max<int64_t>(1, std::min<int64_t>(2 * kWaveItems / seq_rows, ceil_div(tiles, p.min_tiles))));
+        pn.seq_items = seq_rows * p.seq_splits;
+    }
+    p.parts = p.prefix_splits + p.seq_splits;
+    if (p.parts > 1) {
+        pn.lse_bytes = (size_t(p.parts) * d.total_q * d.n_heads * sizeof(float) + 15) / 16 * 16;
+        pn.o_bytes = size_t(p.parts) * d.total_q * d.n_heads * d.head_dim * sizeof(float);
+    }
+    return pn;
+}
+
+}  // namespace
+
+int64_t prefix_attention_bytes(const prefix_attention_desc &d) {
+    const Plan pn = make_plan(d);
+    return static_cast<int64_t>(pn.o_bytes + pn.lse_bytes);
+}
+
+int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int32_t *status, cudaStream_t s) {
+    const Plan pn = make_plan(d);
+    vitk::PrefixArgs a;
+    a.d = d;
+    a.p = pn.p;
+    a.status = status;
+    a.p.part_o = static_cast<float *>(workspace);
+    a.p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pn.o_bytes);
+    const bool bf = d.dtype == VIT_DTYPE_BF16;
+    cudaError_t e = bf ? small<__nv_bfloat16>(a, 0, pn.m_prefix, pn.prefix_items, s)
+                       : small<__half>(a, 0, pn.m_prefix, pn.prefix_items, s);
+    if (e == cudaSuccess)
+        e = bf ? small<__nv_bfloat16>(a, 1, pn.m_seq, pn.seq_items, s) : small<__half>(a, 1, pn.m_seq, pn.seq_items, s);
+    if (e == cudaSuccess && pn.p.parts > 1) {
+        const unsigned grid = static_cast<unsigned>((int64_t(d.n_seq) * d.max_q * d.n_heads + 7) / 8);
+        if (bf) {
+            vitk::prefix_join_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+        } else {
+            vitk::prefix_join_kernel<__half><<<grid, 256, 0, s>>>(a);
+        }
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+}
+
+}  // namespace vith

@@ -1,0 +1,61 @@
+// prefix_attn.h -- what the kernels of prefix_attention share: the call's arguments, the plan made of
+// them on the host, and the work items a CTA reads from both.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/vit_decoder.h"
+
+namespace vitk {
+
+// How the keys of a row are cut into parts. A part is one work item's range of keys for its rows; a
+// row with one part is written directly, with more they meet in the join kernel.
+struct PrefixPlan {
+    int G;                   // query heads per key-value head
+    bool stacked;            // prefix parts take the queries of all sequences stacked; else each
+                             // sequence's items run over its prefix and suffix keys in turn
+    int prefix_splits;       // stacked only: parts of the prefix, tiles_per_split key tiles each
+    int prefix_tiles_per_split;
+    int seq_splits;          // most parts of a sequence's own items (0: none, stacked without a suffix)
+    int min_tiles;           // fewest key tiles of a part of a sequence's items
+    int parts;               // prefix_splits + seq_splits
+    float *part_o;           // fp32 [parts][total_q][n_heads][head_dim], unused with one part
+    float *part_lse;         // fp32 [parts][total_q][n_heads], log2 units
+};
+
+struct PrefixArgs {
+    prefix_attention_desc d;
+    PrefixPlan p;
+    int32_t *status;
+};
+
+// a sequence's query rows and keys, from the device's lengths, kept inside the buffers whatever they say
+struct SeqRange {
+    int64_t q0;
+    int n_q;
+    int len;
+    bool ok;
+};
+__device__ __forceinline__ SeqRange seq_range(const prefix_attention_desc &d, int b) {
+    SeqRange r;
+    int64_t a, e;
+    if (d.cu_q != nullptr) {
+        a = d.cu_q[b];
+        e = d.cu_q[b + 1];
+    } else {
+        a = static_cast<int64_t>(b) * d.max_q;
+        e = a + d.max_q;
+    }
+    r.ok = a >= 0 && e >= a && e <= d.total_q && e - a <= d.max_q;
+    r.q0 = a < 0 ? 0 : (a > d.total_q ? d.total_q : a);
+    int64_t n = (e > d.total_q ? d.total_q : e) - r.q0;
+    n = n < 0 ? 0 : (n > d.max_q ? d.max_q : n);
+    r.n_q = static_cast<int>(n);
+    const int64_t len = d.lens != nullptr ? d.lens[b] : 0;
+    r.ok = r.ok && len >= 0 && len <= d.max_len;
+    r.len = static_cast<int>(len < 0 ? 0 : (len > d.max_len ? d.max_len : len));
+    return r;
+}
+
+}  // namespace vitk

@@ -1,4 +1,5 @@
-"""ctypes binding of ``libvit_b200.so`` (the C ABI in ``include/vit.h`` and ``include/vit_ops.h``).
+"""ctypes binding of ``libvit_b200.so`` (the C ABI in ``include/vit.h``, ``include/vit_ops.h`` and
+``include/vit_decoder.h``).
 
 Argument marshalling only: torch supplies device memory and streams; every step of the encoder
 runs in the library's CUDA kernels. There is no fallback: if the library is missing or the
@@ -6,6 +7,7 @@ device is not an sm_100 GPU, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional, Sequence
@@ -45,6 +47,19 @@ class VitWeightsDesc(ctypes.Structure):
                 ("full_attention", ctypes.POINTER(ctypes.c_uint8)),
                 ("fp8_layers", ctypes.POINTER(VitLayerFp8))]
 
+
+
+class PrefixAttentionDesc(ctypes.Structure):
+    _fields_ = [("dtype", c_int), ("n_heads", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("scale", c_float),
+                ("causal", c_int), ("q", c_void_p), ("q_stride", c_int64), ("out", c_void_p), ("out_stride", c_int64),
+                ("lse", c_void_p), ("total_q", c_int64), ("max_q", c_int64), ("cu_q", c_void_p), ("n_seq", c_int),
+                ("prefix_k", c_void_p), ("prefix_v", c_void_p), ("prefix_len", c_int64),
+                ("prefix_k_token", c_int64), ("prefix_k_head", c_int64), ("prefix_v_token", c_int64),
+                ("prefix_v_head", c_int64), ("k", c_void_p), ("v", c_void_p), ("k_seq", c_int64), ("k_token", c_int64),
+                ("k_head", c_int64), ("v_seq", c_int64), ("v_token", c_int64), ("v_head", c_int64),
+                ("lens", c_void_p), ("max_len", c_int64)]
+
+
 # The Qwen2.5-VL tower's full-attention blocks (0-based) when windows are on
 QWEN25_FULL_BLOCKS = (7, 15, 23, 31)
 
@@ -82,6 +97,21 @@ _SIGS = {
                             c_void_p]),
     "scatter_vision_tokens": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p,
                                       c_void_p, c_void_p]),
+    "mrope_norm_apply": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_int64,
+                                 c_int, c_int, c_int, c_void_p, c_void_p, c_float, c_void_p, c_int64, ctypes.c_double,
+                                 c_i32p, c_void_p]),
+    "mrope_norm_grad_workspace": (c_int64, [c_int]),
+    "mrope_norm_grad": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p, c_int64,
+                                c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                c_void_p, c_float, c_void_p, c_int64, ctypes.c_double, c_i32p, c_void_p, c_int64,
+                                c_void_p]),
+    "embed_vision_tokens": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_int64, c_int, c_float, c_void_p, c_int64,
+                                    c_void_p, c_void_p, c_void_p]),
+    "embed_vision_tokens_grad_workspace": (c_int64, [c_int64, c_int64, c_int]),
+    "embed_vision_tokens_grad": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_int64, c_int, c_float, c_void_p, c_int,
+                                         c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "prefix_attention_workspace": (c_int64, [ctypes.POINTER(PrefixAttentionDesc)]),
+    "prefix_attention": (c_int, [ctypes.POINTER(PrefixAttentionDesc), c_void_p, c_int64, c_void_p, c_void_p]),
     "vit_op_window_positions": (c_int, [c_i32p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                         ctypes.POINTER(c_int), c_void_p]),
     "vit_op_gather_rows": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p]),
@@ -423,6 +453,261 @@ def scatter_vision_tokens(input_ids, embed_table, vision, out=None, status=None,
     check(lib().scatter_vision_tokens(_ptr(input_ids), L, _ptr(embed_table), V, D, _ptr(vision), n_vis, _ptr(out),
                                       _ptr(status), _stream(stream)), "scatter_vision_tokens")
     return out
+
+
+# ------------------------------------------------------------------------------------------------
+# decoder-side steps with their gradients, and attention over a shared prefix (include/vit_decoder.h)
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _place(t: torch.Tensor, stream):
+    """The context a call on ``t`` runs in: t's device current and, where a stream is given, that
+    stream current, so that outputs and workspaces made inside belong to it."""
+    if stream is not None:
+        _need(stream.device == t.device, "the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    return _HERE_AND_NOW if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+
+
+def _same_device(*tensors) -> None:
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        _need(t.is_cuda, "tensors must be on a GPU")
+        _need(dev is None or t.device == dev, "tensors are on different devices")
+        dev = t.device
+
+
+def _heads_arg(x, what: str):
+    """[L, heads, head_dim] with heads contiguous -> (pointer, token stride, heads)."""
+    if x is None:
+        return None, 0, 0
+    _need(x.dim() == 3, f"{what} must be [L, heads, head_dim]")
+    L, H, D = x.shape
+    st = x.stride()
+    _need((st[2] == 1 or D == 1) and (st[1] == D or H == 1), f"{what}: the heads of a token must be contiguous")
+    return x.data_ptr(), (st[0] if L > 1 else H * D), H
+
+
+def _like(x, out, what: str):
+    """``out``, or a new contiguous tensor like x (None for None)."""
+    if x is None:
+        _need(out is None, f"{what} given without its input")
+        return None
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need(out.shape == x.shape and out.dtype == x.dtype, f"{what} must have its input's shape and type")
+    return out
+
+
+def _status_arg(status):
+    if status is not None:
+        _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32 [1]")
+    return _ptr(status)
+
+
+def _norm_args(q, k, pos, q_weight, k_weight, sections):
+    x = q if q is not None else k
+    _need(x is not None, "q or k must be given")
+    _need(q is None or k is None or (q.shape[0] == k.shape[0] and q.shape[2] == k.shape[2] and q.dtype == k.dtype),
+          "q and k must have the same tokens, head_dim and type")
+    _need(x.dtype in DTYPES, "q and k must be bf16, fp16 or fp32")
+    L, D = x.shape[0], x.shape[2]
+    _need(pos.dtype == torch.int32 and pos.shape == (3, L) and pos.is_contiguous(), "pos must be contiguous int32 [3, L]")
+    for w in (q_weight, k_weight):
+        _need(w is None or (w.dtype == x.dtype and w.shape == (D,) and w.is_contiguous()),
+              "weights must be [head_dim] of the type of q and k")
+    _same_device(q, k, pos, q_weight, k_weight)
+    sec = (ctypes.c_int32 * 3)(*(int(v) for v in sections))
+    return x, L, D, DTYPES[x.dtype], sec
+
+
+def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6, theta: float = MROPE_THETA,
+                     sections=MROPE_SECTIONS, q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm and 3-D M-RoPE of q [L, heads, head_dim] and k [L, kv_heads, head_dim] in one
+    pass (either may be None; token strides are free, so slices of a packed QKV product work); weights
+    [head_dim] or None (ones); pos int32 [3, L]. Returns (q_out, k_out): new tensors, or the given
+    ones, which may be q and k themselves."""
+    x, L, D, dt, sec = _norm_args(q, k, pos, q_weight, k_weight, sections)
+    with _place(x, stream):
+        q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
+        _same_device(x, q_out, k_out)
+        qp, qs, H = _heads_arg(q, "q")
+        kp, ks, Hk = _heads_arg(k, "k")
+        qo, qos, _ = _heads_arg(q_out, "q_out")
+        ko, kos, _ = _heads_arg(k_out, "k_out")
+        check(lib().mrope_norm_apply(qp, qs, qo, qos, H, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight), _ptr(k_weight),
+                                     eps, _ptr(pos), L, theta, sec, _stream(None)), "mrope_norm_apply")
+    return q_out, k_out
+
+
+def mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    theta: float = MROPE_THETA, sections=MROPE_SECTIONS, dq=None, dk=None, weight_grads: bool = True,
+                    stream=None):
+    """Gradient of ``mrope_norm_apply`` at the same q, k, weights and positions: (dq, dk, dq_weight,
+    dk_weight), the weights' in fp32 (None with weight_grads False, or for a missing q or k)."""
+    x, L, D, dt, sec = _norm_args(q, k, pos, q_weight, k_weight, sections)
+    for g, t in ((dq_out, q), (dk_out, k)):
+        _need((g is None) == (t is None) and (g is None or (g.shape == t.shape and g.dtype == t.dtype)),
+              "the outputs' gradients must have the shape and type of q and k")
+    with _place(x, stream):
+        dq, dk = _like(q, dq, "dq"), _like(k, dk, "dk")
+        _same_device(x, dq_out, dk_out, dq, dk)
+        dw = [None, None]
+        ws, ws_bytes = None, 0
+        if weight_grads:
+            dw = [None if t is None else torch.empty(D, dtype=torch.float32, device=x.device) for t in (q, k)]
+            ws_bytes = lib().mrope_norm_grad_workspace(D)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+        gq, gqs, _ = _heads_arg(dq_out, "dq_out")
+        gk, gks, _ = _heads_arg(dk_out, "dk_out")
+        qp, qs, H = _heads_arg(q, "q")
+        kp, ks, Hk = _heads_arg(k, "k")
+        qo, qos, _ = _heads_arg(dq, "dq")
+        ko, kos, _ = _heads_arg(dk, "dk")
+        check(lib().mrope_norm_grad(gq, gqs, qp, qs, qo, qos, H, gk, gks, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight),
+                                    _ptr(k_weight), _ptr(dw[0]), _ptr(dw[1]), eps, _ptr(pos), L, theta, sec, _ptr(ws),
+                                    ws_bytes, _stream(None)), "mrope_norm_grad")
+    return dq, dk, dw[0], dw[1]
+
+
+def _ids_arg(input_ids):
+    _need(input_ids.dtype == torch.int32 and input_ids.dim() == 1 and input_ids.is_contiguous(),
+          "input_ids must be contiguous int32 [L]")
+
+
+def embed_vision_tokens(input_ids, embed_table, vision=None, scale: float = 1.0, out=None, status=None, stream=None):
+    """The decoder's input rows: scale * embedding for text ids, vision tokens (unscaled) at the image /
+    video placeholders. bf16, fp16 or fp32, all of one type."""
+    _ids_arg(input_ids)
+    L, (V, D) = input_ids.shape[0], embed_table.shape
+    _need(embed_table.dtype in DTYPES and embed_table.is_contiguous(), "embed_table must be contiguous bf16, fp16 or fp32")
+    n_vis = 0 if vision is None else vision.shape[0]
+    _need(vision is None or (vision.dtype == embed_table.dtype and vision.shape == (n_vis, D) and vision.is_contiguous()),
+          "vision must be contiguous [n_vision, dim] of the table's type")
+    with _place(embed_table, stream):
+        if out is None:
+            out = torch.empty((L, D), dtype=embed_table.dtype, device=embed_table.device)
+        _need(out.shape == (L, D) and out.dtype == embed_table.dtype and out.is_contiguous(),
+              "out must be contiguous [L, dim] of the table's type")
+        _same_device(input_ids, embed_table, vision, out, status)
+        check(lib().embed_vision_tokens(_ptr(input_ids), L, _ptr(embed_table), DTYPES[embed_table.dtype], V, D, scale,
+                                        _ptr(vision) if n_vis else None, n_vis, _ptr(out), _status_arg(status),
+                                        _stream(None)), "embed_vision_tokens")
+    return out
+
+
+def embed_vision_tokens_grad(input_ids, d_out, vocab: int, n_vision: int = 0, scale: float = 1.0, table_dtype=None,
+                             d_table=None, accumulate: bool = False, d_vision=None, status=None, stream=None):
+    """Gradient of ``embed_vision_tokens``: (d_table [vocab, dim], d_vision [n_vision, dim] or None). d_table
+    is of table_dtype (d_out's type, or fp32); a given d_table is overwritten, or added to with
+    accumulate (then only the rows that input_ids names are touched)."""
+    _ids_arg(input_ids)
+    L = input_ids.shape[0]
+    _need(d_out.dtype in DTYPES and d_out.dim() == 2 and d_out.shape[0] == L and d_out.is_contiguous(),
+          "d_out must be contiguous [L, dim] in bf16, fp16 or fp32")
+    D = d_out.shape[1]
+    _need(d_table is not None or not accumulate, "accumulate needs a d_table to add to")
+    if table_dtype is None:
+        table_dtype = d_out.dtype if d_table is None else d_table.dtype
+    _need(table_dtype in (d_out.dtype, torch.float32), "the table's gradient is of d_out's type or fp32")
+    with _place(d_out, stream):
+        if d_table is None:
+            d_table = torch.empty((vocab, D), dtype=table_dtype, device=d_out.device)
+        _need(d_table.shape == (vocab, D) and d_table.dtype == table_dtype and d_table.is_contiguous(),
+              "d_table must be contiguous [vocab, dim] of table_dtype")
+        if d_vision is None and n_vision:
+            d_vision = torch.empty((n_vision, D), dtype=d_out.dtype, device=d_out.device)
+        _need(d_vision is None or (d_vision.shape == (n_vision, D) and d_vision.dtype == d_out.dtype
+                                   and d_vision.is_contiguous()),
+              "d_vision must be contiguous [n_vision, dim] of d_out's type")
+        _same_device(input_ids, d_out, d_table, d_vision, status)
+        ws_bytes = lib().embed_vision_tokens_grad_workspace(L, vocab, D)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=d_out.device)
+        check(lib().embed_vision_tokens_grad(_ptr(input_ids), L, _ptr(d_out), DTYPES[d_out.dtype], vocab, D, scale,
+                                             _ptr(d_table), DTYPES[table_dtype], 1 if accumulate else 0,
+                                             _ptr(d_vision), n_vision, _ptr(ws), ws_bytes, _status_arg(status),
+                                             _stream(None)), "embed_vision_tokens_grad")
+    return d_table, d_vision
+
+
+def prefix_attention(q, prefix_k=None, prefix_v=None, k=None, v=None, lens=None, cu_q=None, max_q: Optional[int] = None,
+                     max_len: Optional[int] = None, scale: Optional[float] = None, causal: bool = True, out=None,
+                     lse=None, status=None, stream=None):
+    """Attention of a batch of sequences over a prefix they share and over keys of their own.
+
+    q [total_q, heads, head_dim]: the sequences' queries one after another, cu_q int32 [n_seq + 1]
+    their first rows (None: max_q each); prefix_k, prefix_v [prefix_len, kv_heads, head_dim] or None;
+    k, v [n_seq, capacity, kv_heads, head_dim] with lens int32 [n_seq] keys in use, or None; any strides
+    with contiguous head_dim (head-major caches as permuted views). cu_q and lens are read on the device.
+    max_q defaults to 1 without cu_q, else to total_q; max_len to the capacity. With ``causal`` query j
+    of n sees its sequence's keys s <= lens - n + j. Returns (out, lse): out like q, lse fp32 [total_q, heads]."""
+    _need(q.dim() == 3 and q.dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16 [total_q, heads, head_dim]")
+    T, H, D = q.shape
+    _need((prefix_k is None) == (prefix_v is None) and (k is None) == (v is None), "keys and values go together")
+    _need(prefix_k is not None or k is not None, "a prefix or own keys must be given")
+    _need((k is None) == (lens is None), "own keys need their lengths")
+    Hk = (prefix_k if prefix_k is not None else k).shape[-2]
+    d = PrefixAttentionDesc()
+    if prefix_k is not None:
+        Lp = prefix_k.shape[0]
+        for t in (prefix_k, prefix_v):
+            _need(t.shape == (Lp, Hk, D) and t.dtype == q.dtype and (t.stride(2) == 1 or D == 1),
+                  "prefix keys and values must be [prefix_len, kv_heads, head_dim] of q's type, head_dim contiguous")
+        d.prefix_len = Lp
+        if Lp:
+            d.prefix_k, d.prefix_v = prefix_k.data_ptr(), prefix_v.data_ptr()
+            (d.prefix_k_token, d.prefix_k_head, _), (d.prefix_v_token, d.prefix_v_head, _) = prefix_k.stride(), prefix_v.stride()
+    if k is not None:
+        B, cap = k.shape[0], k.shape[1]
+        for t in (k, v):
+            _need(t.shape == (B, cap, Hk, D) and t.dtype == q.dtype and (t.stride(3) == 1 or D == 1),
+                  "own keys and values must be [n_seq, capacity, kv_heads, head_dim] of q's type, head_dim contiguous")
+        _need(lens.dtype == torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [n_seq]")
+        max_len = cap if max_len is None else max_len
+        _need(0 <= max_len <= cap, "max_len must be within the capacity")
+        if cap:
+            d.k, d.v, d.lens, d.max_len = k.data_ptr(), v.data_ptr(), lens.data_ptr(), max_len
+            (d.k_seq, d.k_token, d.k_head, _), (d.v_seq, d.v_token, d.v_head, _) = k.stride(), v.stride()
+    if cu_q is not None:
+        _need(cu_q.dtype == torch.int32 and cu_q.dim() == 1 and cu_q.shape[0] >= 2 and cu_q.is_contiguous(),
+              "cu_q must be int32 [n_seq + 1]")
+        n_seq = cu_q.shape[0] - 1
+        max_q = max(T, 1) if max_q is None else max_q
+        d.cu_q = cu_q.data_ptr()
+    else:
+        max_q = 1 if max_q is None else max_q
+        n_seq = k.shape[0] if k is not None else T // max(max_q, 1)
+        _need(n_seq * max_q == T or T == 0, "without cu_q there must be max_q queries for each sequence")
+    _need(k is None or k.shape[0] == n_seq, "k and cu_q disagree on the number of sequences")
+    with _place(q, stream):
+        if out is None:
+            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        _need(out.shape == q.shape and out.dtype == q.dtype, "out must have q's shape and type")
+        _need(lse.shape == (T, H) and lse.dtype == torch.float32 and lse.is_contiguous(), "lse must be fp32 [total_q, heads]")
+        _same_device(q, prefix_k, prefix_v, k, v, lens, cu_q, out, lse, status)
+        if T == 0:
+            return out, lse
+        d.dtype, d.n_heads, d.n_kv_heads, d.head_dim = DTYPES[q.dtype], H, Hk, D
+        d.scale, d.causal = (D ** -0.5 if scale is None else scale), 1 if causal else 0
+        d.q, d.q_stride, _ = _heads_arg(q, "q")
+        d.out, d.out_stride, _ = _heads_arg(out, "out")
+        d.lse, d.total_q, d.max_q, d.n_seq = lse.data_ptr(), T, max_q, n_seq
+        L = lib()
+        ws_bytes = L.prefix_attention_workspace(ctypes.byref(d))
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+        check(L.prefix_attention(ctypes.byref(d), _ptr(ws), ws_bytes, _status_arg(status), _stream(None)),
+              "prefix_attention")
+    return out, lse
 
 
 def op_wait_selftest(status, limit_cycles: int, stream=None):
