@@ -30,6 +30,13 @@ int tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int e
             uint64_t outer, uint64_t row_pitch_bytes, uint32_t box_inner, uint32_t box_outer,
             CUtensorMapSwizzle swizzle) {
     (void)elem_bytes;
+    const uint64_t dims[2] = {inner, outer}, strides[1] = {row_pitch_bytes};
+    const uint32_t box[2] = {box_inner, box_outer};
+    return tmap_nd(map, base, dtype, 2, dims, strides, box, swizzle);
+}
+
+int tmap_nd(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank, const uint64_t *dims,
+            const uint64_t *stride_bytes, const uint32_t *box, CUtensorMapSwizzle swizzle) {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -38,11 +45,15 @@ int tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int e
             g_encode = reinterpret_cast<EncodeTiledFn>(fn);
     });
     if (!g_encode) return VIT_ERR_CUDA;
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {row_pitch_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr,
+    cuuint64_t gdims[5], strides[4];
+    cuuint32_t gbox[5], estr[5];
+    for (int i = 0; i < rank; ++i) {
+        gdims[i] = dims[i];
+        gbox[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) strides[i] = stride_bytes[i];
+    }
+    CUresult r = g_encode(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void *>(base), gdims, strides, gbox, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? VIT_OK : VIT_ERR_CUDA;

@@ -41,6 +41,10 @@ int tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int e
             uint64_t outer, uint64_t row_pitch_bytes, uint32_t box_inner, uint32_t box_outer,
             CUtensorMapSwizzle swizzle);
 
+// rank 2..5; dims, box: rank entries; stride_bytes: rank - 1 entries (dimension 0 is contiguous)
+int tmap_nd(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int rank, const uint64_t *dims,
+            const uint64_t *stride_bytes, const uint32_t *box, CUtensorMapSwizzle swizzle);
+
 int device_sm_count();
 int check_device();   // VIT_OK when the current device is sm_100
 

@@ -398,7 +398,11 @@ void fill(vitk::NormRopeArgs &a, const NormRopeCall &c, int tile) {
     a.n_freq = c.head_dim / 2;
     a.axis_end0 = c.sections[0];
     a.axis_end1 = c.sections[0] + c.sections[1];
-    for (int j = 0; j < a.n_freq; ++j) a.inv_freq[j] = std::pow(c.theta, -2.0 * j / c.head_dim);
+    // powers of theta^(-2/D), one product each: j roundings of 2^-53, under 2e-14 relative at j = 128
+    // (10^-9 rad at position 10^5), where one pow per frequency would cost a call 2 us on the host
+    const double step = std::pow(c.theta, -2.0 / c.head_dim);
+    double f = 1.0;
+    for (int j = 0; j < a.n_freq; ++j, f *= step) a.inv_freq[j] = f;
 }
 
 size_t angle_bytes(int tile, int D) { return sizeof(float) * (static_cast<size_t>(tile) * D + 2 * D); }

@@ -27,7 +27,6 @@
 namespace vitk {
 
 constexpr int kSmThreads = 128, kSmKeys = 64, kSmStages = 3;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -62,12 +61,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_mufu(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Shared bytes of a key (or value) row: 16 more than the head, an odd number of 16-byte words, so the
 // eight rows of an ldmatrix fall into different banks.
 template <int DP>
@@ -365,8 +358,6 @@ namespace vith {
 
 namespace {
 
-constexpr int kWaveItems = 148 * 2;       // CTAs resident at a time
-
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 template <typename T, int DP, int WR, int WK>
@@ -399,10 +390,54 @@ cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, cud
     return small<T, 128>(a, kind, m, items, s);
 }
 
+// One kind of work item: which kernel takes it and how its keys are cut.
+struct Items {
+    int m = 0;              // query rows per item: 16 or 64 (small kernel), kTcRows (tensor-core kernel)
+    int keys = 0;           // keys per tile
+    int splits = 0;         // parts of the keys
+    int tiles_per_split = 0;
+    int64_t count = 0;
+};
+
+// Up to 64 rows the small kernel: below that its tiles are as fast as their keys arrive (a 64-key tile of
+// 128 dims is 32 KB, 1.5 us of a CTA's share of HBM), the tensor-core kernel would run its 128-row tiles
+// mostly empty.
+Items shape(int64_t rows) {
+    Items it;
+    it.m = rows <= 16 ? 16 : rows <= 64 ? 64 : kTcRows;
+    it.keys = it.m == kTcRows ? kTcKeys : vitk::kSmKeys;
+    return it;
+}
+
+// Cuts the keys of `base` items of `tiles` tiles each so that the waves of CTAs (one per SM of the
+// tensor-core kernel, two of the small one) fill up, against what the parts cost: with more than one, every part writes
+// and the join reads an fp32 row of o, and the join is one more launch (about 4 us).
+void cut(Items &it, int64_t base, int tiles, int64_t part_row_bytes, bool joined, int max_splits) {
+    const bool tc = it.m == kTcRows;
+    const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;
+    const int64_t wave = tc ? 148 : 296;
+    double best = 1e30;
+    int pick = 1;
+    for (int s = 1; s <= std::min(tiles, max_splits); ++s) {
+        const int per = ceil_div(tiles, s);
+        if (s > 1 && ceil_div(tiles, per) != s) continue;      // the same parts as a smaller s
+        const double waves = static_cast<double>((base * s + wave - 1) / wave);
+        double us = waves * (per * tile_us + start_us);
+        if (joined || s > 1) us += s * part_row_bytes * 2 / 4.0e6;
+        if (!joined && s > 1) us += 4.0;
+        if (us < best * 0.98) {
+            best = us;
+            pick = s;
+        }
+    }
+    it.splits = pick;
+    it.tiles_per_split = ceil_div(std::max(tiles, 1), pick);
+    it.count = base * pick;
+}
+
 struct Plan {
     vitk::PrefixPlan p;
-    int m_prefix, m_seq;                  // row tiles of the two kinds of items
-    int64_t prefix_items, seq_items;
+    Items prefix, seq;
     size_t o_bytes, lse_bytes;
 };
 
@@ -411,31 +446,43 @@ Plan make_plan(const prefix_attention_desc &d) {
     vitk::PrefixPlan &p = pn.p;
     p.G = d.n_heads / d.n_kv_heads;
     const bool own = d.k != nullptr && d.max_len > 0;
-    const int prefix_tiles = ceil_div(d.prefix_len, vitk::kSmKeys), own_tiles = own ? ceil_div(d.max_len, vitk::kSmKeys) : 0;
-    pn.m_seq = d.max_q * p.G <= 16 ? 16 : 64;
-    pn.m_prefix = d.total_q * p.G <= 16 ? 16 : 64;
-    p.stacked = d.n_seq > 1 && prefix_tiles > 0 && d.total_q * p.G < int64_t(d.n_seq) * 64;
-    p.min_tiles = 4;
-    const int64_t seq_rows = int64_t(d.n_seq) * d.n_kv_heads * ceil_div(d.max_q * p.G, pn.m_seq);
+    const int64_t max_rows = d.max_q * p.G, rows = d.total_q * p.G;
+    const int64_t part_row_bytes = d.total_q * d.n_heads * d.head_dim * int64_t(sizeof(float));
+    // Stacked or not, in tiles of 256 rows x 80 keys: stacking reads the prefix once for rows of all
+    // sequences but leaves two parts per row to join, whose fp32 rows cost about 12 tiles per 256 rows.
+    const int64_t pre80 = ceil_div(d.prefix_len, kTcKeys), own80 = own ? ceil_div(d.max_len, kTcKeys) : 0;
+    const int64_t seq_tiles = d.n_seq * int64_t(ceil_div(ceil_div(rows, d.n_seq), kTcRows)), all_tiles = ceil_div(rows, kTcRows);
+    p.stacked = d.n_seq > 1 && d.prefix_len > 0 &&
+                all_tiles * pre80 + seq_tiles * own80 + 12 * all_tiles < seq_tiles * (pre80 + own80);
+    const bool two_kinds = p.stacked && own;
     if (p.stacked) {
-        const int64_t rows = int64_t(d.n_kv_heads) * ceil_div(d.total_q * p.G, pn.m_prefix);
-        int64_t splits = std::max<int64_t>(1, std::min<int64_t>(kWaveItems / rows, prefix_tiles / p.min_tiles));
-        p.prefix_tiles_per_split = ceil_div(prefix_tiles, splits);
-        p.prefix_splits = ceil_div(prefix_tiles, p.prefix_tiles_per_split);
-        pn.prefix_items = rows * p.prefix_splits;
+        pn.prefix = shape(rows);
+        cut(pn.prefix, int64_t(d.n_kv_heads) * ceil_div(rows, pn.prefix.m), ceil_div(d.prefix_len, pn.prefix.keys),
+            part_row_bytes, two_kinds, 64);
+        p.prefix_splits = pn.prefix.splits;
+        p.prefix_tiles_per_split = pn.prefix.tiles_per_split;
     }
-    const int tiles = own_tiles + (p.stacked ? 0 : prefix_tiles);
     if (!p.stacked || own) {
-        p.seq_splits = static_cast<int>(
-            std::max<int64_t>(1, std::min<int64_t>(2 * kWaveItems / seq_rows, ceil_div(tiles, p.min_tiles))));
-        pn.seq_items = seq_rows * p.seq_splits;
+        pn.seq = shape(max_rows);
+        const int tiles = (own ? ceil_div(d.max_len, pn.seq.keys) : 0) + (p.stacked ? 0 : ceil_div(d.prefix_len, pn.seq.keys));
+        cut(pn.seq, int64_t(d.n_seq) * d.n_kv_heads * ceil_div(max_rows, pn.seq.m), tiles, part_row_bytes, two_kinds, 64);
+        p.seq_splits = pn.seq.splits;
+        p.min_tiles = pn.seq.splits > 1 ? 2 : 1;
     }
     p.parts = p.prefix_splits + p.seq_splits;
     if (p.parts > 1) {
         pn.lse_bytes = (size_t(p.parts) * d.total_q * d.n_heads * sizeof(float) + 15) / 16 * 16;
-        pn.o_bytes = size_t(p.parts) * d.total_q * d.n_heads * d.head_dim * sizeof(float);
+        pn.o_bytes = size_t(p.parts) * part_row_bytes;
     }
     return pn;
+}
+
+int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, cudaStream_t s) {
+    if (it.count <= 0) return VIT_OK;
+    if (it.m == kTcRows) return prefix_tc_launch(a, kind, it.count, s);
+    const cudaError_t e = a.d.dtype == VIT_DTYPE_BF16 ? small<__nv_bfloat16>(a, kind, it.m, it.count, s)
+                                                      : small<__half>(a, kind, it.m, it.count, s);
+    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
 }  // namespace
@@ -453,21 +500,16 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     a.status = status;
     a.p.part_o = static_cast<float *>(workspace);
     a.p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pn.o_bytes);
-    const bool bf = d.dtype == VIT_DTYPE_BF16;
-    cudaError_t e = bf ? small<__nv_bfloat16>(a, 0, pn.m_prefix, pn.prefix_items, s)
-                       : small<__half>(a, 0, pn.m_prefix, pn.prefix_items, s);
-    if (e == cudaSuccess)
-        e = bf ? small<__nv_bfloat16>(a, 1, pn.m_seq, pn.seq_items, s) : small<__half>(a, 1, pn.m_seq, pn.seq_items, s);
-    if (e == cudaSuccess && pn.p.parts > 1) {
-        const unsigned grid = static_cast<unsigned>((int64_t(d.n_seq) * d.max_q * d.n_heads + 7) / 8);
-        if (bf) {
-            vitk::prefix_join_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-        } else {
-            vitk::prefix_join_kernel<__half><<<grid, 256, 0, s>>>(a);
-        }
-        e = cudaGetLastError();
+    int rc = run_items(a, 0, pn.prefix, s);
+    if (rc == VIT_OK) rc = run_items(a, 1, pn.seq, s);
+    if (rc != VIT_OK || pn.p.parts == 1) return rc;
+    const unsigned grid = static_cast<unsigned>((int64_t(d.n_seq) * d.max_q * d.n_heads + 7) / 8);
+    if (d.dtype == VIT_DTYPE_BF16) {
+        vitk::prefix_join_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    } else {
+        vitk::prefix_join_kernel<__half><<<grid, 256, 0, s>>>(a);
     }
-    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
 }  // namespace vith

@@ -9,6 +9,14 @@
 
 namespace vitk {
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_mufu(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // How the keys of a row are cut into parts. A part is one work item's range of keys for its rows; a
 // row with one part is written directly, with more they meet in the join kernel.
 struct PrefixPlan {
@@ -59,3 +67,10 @@ __device__ __forceinline__ SeqRange seq_range(const prefix_attention_desc &d, in
 }
 
 }  // namespace vitk
+
+namespace vith {
+// The tensor-core kernel (prefix_tc.cu) over `items` work items of `kind` (as prefix_small_kernel's),
+// kTcRows query rows each, in tiles of kTcKeys keys.
+constexpr int kTcRows = 256, kTcKeys = 80;
+int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s);
+}  // namespace vith

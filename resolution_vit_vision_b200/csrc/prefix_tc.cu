@@ -1,0 +1,453 @@
+// prefix_tc.cu -- prefix_attention for many query rows per key: the tcgen05 tensor-core kernel.
+//
+// A work item is 256 query rows of one key-value head (a row is a token and one of its G query heads:
+// the queries of the whole batch stacked for the prefix part, or one sequence's) against a range of
+// key tiles, a prefix's and then the sequence's own. The two products of a tile are bound by the
+// softmax between them: per (row, key) one exponential on the MUFU and about five issue slots against
+// 4 head_dim tensor-core FLOPs. So two 128-row tiles A and B share every K / V tile and take turns:
+//   warp 0      TMA producer: K_j and V_j (64-column boxes, 128-byte swizzle; head dims behind head_dim
+//               and keys behind the prefix arrive as zeros) into a 4-deep ring
+//   warps 1, 2  one MMA-issuing warp per query tile: S_x(j) = Q_x K_j^T (M 128, N 80) into tensor memory,
+//               O_x += P_x(j) V_j with P_x from tensor memory; S_x(j + 1) is issued as soon as the
+//               softmax has read S_x(j), so the next scores wait for the softmax and not the reverse
+//   warps 3..10 softmax, one row per thread: online maximum with a lazy rescale (the exponent offset moves
+//               only when the maximum grows by more than 2^8), fp32 sums, P rounded to the element type
+// Tensor memory: S and P of both tiles beside two 128-column accumulators leave room for 80 keys per
+// tile (2 x (80 + 40) + 2 x 128 columns of 512). Q is copied by the softmax warps (rows of any token
+// and head, so 256 rows are filled whatever G is).
+// Own keys behind a sequence's length may hold anything: their scores are masked by row, and the
+// issuing warps zero their V rows in shared memory first (0 x NaN would reach every row).
+#include <algorithm>
+
+#include "dtype.cuh"
+#include "internal.h"
+#include "prefix_attn.h"
+#include "ptx.cuh"
+
+namespace vitk {
+
+constexpr int kTcThreads = 352, kTcStages = 4, kTcNK = vith::kTcKeys, kTcM = 128;
+constexpr int kTcQBox = kTcM * 128;                  // 128 rows x 64 columns
+constexpr int kTcKBox = kTcNK * 128;                 // 80 keys x 64 columns
+template <int HV>                                    // 64-column halves of a head: head_dim <= 64 HV
+constexpr int kTcSmem = 1024 + 2 * HV * kTcQBox + kTcStages * 2 * HV * kTcKBox + 256;
+constexpr float kTcRescale = 8.0f;
+
+__device__ __forceinline__ uint32_t tc_s(int x) { return x * 80; }
+__device__ __forceinline__ uint32_t tc_p(int x) { return 160 + x * 40; }
+__device__ __forceinline__ uint32_t tc_o(int x) { return 256 + x * 128; }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+template <typename T>
+struct MmaType;
+template <>
+struct MmaType<__nv_bfloat16> {
+    static constexpr uint32_t kCode = 1;
+};
+template <>
+struct MmaType<__half> {
+    static constexpr uint32_t kCode = 0;
+};
+
+template <typename T, int HV>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tpk, const __grid_constant__ CUtensorMap tpv,
+                     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                     const __grid_constant__ PrefixArgs a, int kind) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int kQTile = HV * kTcQBox, kTile = HV * kTcKBox;
+    uint8_t *sQ = smem;                                   // [2][HV] boxes
+    uint8_t *sK = sQ + 2 * kQTile;                        // [stages][HV]
+    uint8_t *sV = sK + kTcStages * kTile;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sV + kTcStages * kTile);
+    uint64_t *k_full = bars;
+    uint64_t *v_full = k_full + kTcStages;
+    uint64_t *kv_empty = v_full + kTcStages;
+    uint64_t *q_full = kv_empty + kTcStages;              // [2] per query tile, as the rest
+    uint64_t *s_full = q_full + 2;
+    uint64_t *s_free = s_full + 2;
+    uint64_t *p_full = s_free + 2;
+    uint64_t *o_done = p_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_done + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const prefix_attention_desc &d = a.d;
+    const PrefixPlan &pl = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int D = d.head_dim, G = pl.G;
+
+    // ---- the item (as prefix_small_kernel's)
+    const int h = blockIdx.x % d.n_kv_heads;
+    int rest = blockIdx.x / d.n_kv_heads;
+    int64_t q0;
+    int n_q, len = 0, b = 0, part, row0, t0, t1, n_prefix_tiles, own_keys = 0;
+    const int prefix_tiles = static_cast<int>((d.prefix_len + kTcNK - 1) / kTcNK);
+    if (kind == 0) {
+        part = rest % pl.prefix_splits;
+        row0 = rest / pl.prefix_splits * vith::kTcRows;
+        q0 = 0;
+        n_q = static_cast<int>(d.total_q);
+        n_prefix_tiles = prefix_tiles;
+        t0 = part * pl.prefix_tiles_per_split;
+        t1 = min(prefix_tiles, t0 + pl.prefix_tiles_per_split);
+    } else {
+        const int sp = rest % pl.seq_splits;
+        rest /= pl.seq_splits;
+        const int row_tiles = static_cast<int>((d.max_q * G + vith::kTcRows - 1) / vith::kTcRows);
+        row0 = rest % row_tiles * vith::kTcRows;
+        b = rest / row_tiles;
+        const SeqRange r = seq_range(d, b);
+        if (!r.ok && threadIdx.x == 0 && a.status) atomicExch(a.status, VIT_ERR_LIMIT);
+        q0 = r.q0;
+        n_q = r.n_q;
+        len = r.len;
+        if (row0 >= n_q * G) return;
+        n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
+        part = pl.prefix_splits + sp;
+        own_keys = len;
+        if (d.causal) own_keys = max(0, min(len, len - n_q + min(n_q - 1, (row0 + vith::kTcRows - 1) / G) + 1));
+        const int total = n_prefix_tiles + (own_keys + kTcNK - 1) / kTcNK;
+        const int per = max(pl.min_tiles, (total + pl.seq_splits - 1) / pl.seq_splits);
+        t0 = min(total, sp * per);
+        t1 = min(total, t0 + per);
+    }
+    const int rows = min(vith::kTcRows, n_q * G - row0);
+    const int n_kv = t1 - t0;
+    const int n_x = rows > kTcM ? 2 : 1;                  // query tiles with rows
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kTcStages; ++s) {
+            mbar_init(k_full + s, 1);
+            mbar_init(v_full + s, 1);
+            mbar_init(kv_empty + s, n_x);                 // released by each active tile's issuer
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(q_full + x, kTcM);
+            mbar_init(s_full + x, 1);
+            mbar_init(s_free + x, kTcM);
+            mbar_init(p_full + x, kTcM);
+            mbar_init(o_done + x, 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx wc{abort_flag, a.status};
+    auto tile_key = [&](int t) { return (t < n_prefix_tiles ? t : t - n_prefix_tiles) * kTcNK; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < n_kv; ++i) {
+                const int st = i % kTcStages, t = t0 + i, k0 = tile_key(t);
+                const bool pre = t < n_prefix_tiles;
+                if (!mbar_wait(kv_empty + st, ((i / kTcStages) & 1) ^ 1u, wc)) break;
+                mbar_expect_tx(k_full + st, kTile);
+                for (int c = 0; c < HV; ++c)
+                    tma_load_4d(sK + st * kTile + c * kTcKBox, pre ? &tpk : &tk, k_full + st, c * 64, h, k0, pre ? 0 : b);
+                mbar_expect_tx(v_full + st, kTile);
+                for (int c = 0; c < HV; ++c)
+                    tma_load_4d(sV + st * kTile + c * kTcKBox, pre ? &tpv : &tv, v_full + st, c * 64, h, k0, pre ? 0 : b);
+            }
+        }
+    } else if (warp == 1 || warp == 2) {
+        const int x = warp - 1;
+        if (x < n_x && n_kv > 0) {
+            const int ks = (D + 15) / 16;                 // 16-column steps of the head
+            const uint32_t idS = idesc_f16(MmaType<T>::kCode, kTcM, kTcNK, false);
+            const uint32_t idO = idesc_f16(MmaType<T>::kCode, kTcM, ks * 16, true);
+            const uint32_t qa = smem_u32(sQ) + x * kQTile, ka = smem_u32(sK), va = smem_u32(sV);
+            auto issue_s = [&](int i) {                   // S_x = Q_x K^T
+                const int st = i % kTcStages;
+                for (int c = 0; c < ks; ++c) {
+                    const uint32_t at = (c & 3) * 32;
+                    mma_bf16_ss(tmem + tc_s(x), smem_desc(qa + (c >> 2) * kTcQBox + at, 16, 1024, kSwizzle128B),
+                                smem_desc(ka + st * kTile + (c >> 2) * kTcKBox + at, 16, 1024, kSwizzle128B), idS,
+                                c > 0 ? 1u : 0u);
+                }
+                mma_commit(s_full + x);
+            };
+            auto issue_pv = [&](int i) {                  // O_x += P_x V
+                const int st = i % kTcStages;
+#pragma unroll
+                for (int kk = 0; kk < kTcNK / 16; ++kk)
+                    mma_bf16_ts(tmem + tc_o(x), tmem + tc_p(x) + kk * 8,
+                                smem_desc(va + st * kTile + kk * 2048, kTcKBox, 1024, kSwizzle128B), idO,
+                                (i > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(o_done + x);
+                mma_commit(kv_empty + st);
+            };
+            auto wait_k = [&](int i) { return mbar_wait(k_full + i % kTcStages, (i / kTcStages) & 1, wc); };
+            bool ok = mbar_wait(q_full + x, 0, wc) && wait_k(0);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (ok && lane == 0) issue_s(0);
+            for (int i = 0; ok && i < n_kv; ++i) {
+                const int st = i % kTcStages;
+                if (i + 1 < n_kv) {
+                    ok = mbar_wait(s_free + x, i & 1, wc) && wait_k(i + 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) issue_s(i + 1);
+                }
+                ok = mbar_wait(v_full + st, (i / kTcStages) & 1, wc);
+                const int t = t0 + i, valid = t < n_prefix_tiles ? kTcNK : own_keys - tile_key(t);
+                if (ok && valid < kTcNK) {                // own keys behind the last: zero their V rows
+                    for (int e = lane; e < (kTcNK - valid) * HV * 8; e += 32) {
+                        const int r = valid + e / (HV * 8), c = e % (HV * 8);
+                        *reinterpret_cast<uint4 *>(sV + st * kTile + (c >> 3) * kTcKBox + r * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                ok = ok && mbar_wait(p_full + x, i & 1, wc);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) issue_pv(i);
+                __syncwarp();
+            }
+        }
+    } else if (warp < 3 + 4 * n_x) {
+        const int x = (warp - 3) >> 2;
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;                // row inside the tile
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tS = tmem + tc_s(x) + lane_off, tP = tmem + tc_p(x) + lane_off, tO = tmem + tc_o(x) + lane_off;
+        const T *q = static_cast<const T *>(d.q);
+        {   // Q rows into the swizzled layout of the products: 16-byte word c of row i goes to c ^ (i & 7)
+            constexpr int kWords = HV * 8, kRowsAtOnce = 32 / kWords;
+            const int c = lane % kWords;
+#pragma unroll 8
+            for (int i0 = 0; i0 < 32; i0 += kRowsAtOnce) {
+                const int i = quarter * 32 + i0 + lane / kWords, row = x * kTcM + i;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < rows && c * 8 < D) {
+                    const int R = row0 + row;
+                    v = *reinterpret_cast<const uint4 *>(q + (q0 + R / G) * d.q_stride + (h * G + R % G) * D + c * 8);
+                }
+                *reinterpret_cast<uint4 *>(sQ + x * kQTile + (c >> 3) * kTcQBox + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(q_full + x);
+        }
+        const int R = row0 + x * kTcM + r;
+        const int j = R / G;
+        const int lim = kind == 0 ? 0 : (d.causal ? min(len, len - n_q + j + 1) : len);
+        const float scale_log2 = d.scale * kLog2e;
+        float m_used = -INFINITY, l = 0.f;
+        bool ok = true;
+        // the two groups take turns at the exponentials (named barriers 2 and 3), so one group's loads,
+        // maxima and stores run while the other keeps the MUFU busy; B opens A's first turn
+        const int my_turn = 2 + x, their_turn = 3 - x;
+        if (n_x == 2 && x == 1 && n_kv > 0) named_bar_arrive(2, 256);
+        for (int i = 0; i < n_kv; ++i) {
+            // a wait that timed out does not leave the loop: both groups keep taking their turns
+            if (!mbar_wait(s_full + x, i & 1, wc)) ok = false;
+            __syncwarp();
+            tc_fence_after();
+            uint32_t sr[kTcNK];
+            tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(sr));
+            tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
+            tmem_ld16(tS + 64, sr + 64);
+            tmem_wait_ld();
+            reg_fence32(sr);
+            reg_fence32(sr + 32);
+            reg_fence16(sr + 64);
+            tc_fence_before();
+            mbar_arrive(s_free + x);
+            const int t = t0 + i, k0 = tile_key(t);
+            const int valid = t < n_prefix_tiles ? static_cast<int>(min(static_cast<int64_t>(kTcNK), d.prefix_len - k0)) : lim - k0;
+            if (__any_sync(0xffffffffu, valid < kTcNK)) {
+#pragma unroll
+                for (int k = 0; k < kTcNK; ++k)
+                    if (k >= valid) sr[k] = __float_as_uint(-INFINITY);
+            }
+            float m8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(sr[e]);
+#pragma unroll
+            for (int k = 8; k + 16 <= kTcNK; k += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], __uint_as_float(sr[k + e]), __uint_as_float(sr[k + 8 + e]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], __uint_as_float(sr[kTcNK - 8 + e]));
+            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale_log2;
+            const bool need = mx > m_used + kTcRescale;
+            const float alpha = (i > 0 && need) ? exp2_mufu(m_used - mx) : 1.0f;
+            l *= alpha;
+            if (need) m_used = mx;
+            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;   // no visible key yet: every p stays 0
+            float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[kTcNK / 2];
+            if (n_x == 2) named_bar_sync(my_turn, 256);
+#pragma unroll
+            for (int k = 0; k < kTcNK; k += 8) {
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = fmaf(__uint_as_float(sr[k + e]), scale_log2, neg_m);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = exp2_mufu(p[e]);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    r8[(e >> 1) + 4 * ((k >> 3) & 1)] += p[e] + p[e + 1];
+                    pk[(k + e) >> 1] = pack2(p[e], p[e + 1], T());
+                }
+            }
+            if (n_x == 2 && (x == 0 || i + 1 < n_kv)) named_bar_arrive(their_turn, 256);
+            l += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
+            // P_x V of the tile before must be complete before O_x is scaled or P_x overwritten
+            if (i > 0) {
+                if (!mbar_wait(o_done + x, (i - 1) & 1, wc)) ok = false;
+                __syncwarp();
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c, o);
+                        tmem_wait_ld();
+                        reg_fence16(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st16(tO + c, o);
+                    }
+                }
+            }
+            tmem_st32(tP, pk);
+            tmem_st8(tP + 32, pk + 32);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full + x);
+        }
+        if (n_kv > 0) ok = mbar_wait(o_done + x, (n_kv - 1) & 1, wc) && ok;
+        tc_fence_after();
+        const int64_t token = q0 + j;
+        const int head = h * G + R % G;
+        bool live = ok && R < row0 + rows;
+        if (kind == 0 && pl.parts == 1 && d.cu_q != nullptr) live = live && token < d.cu_q[d.n_seq];
+        const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+        const float lse2 = (m_used == -INFINITY ? 0.f : m_used) + log2f(l);
+        const int64_t prow = (static_cast<int64_t>(part) * d.total_q + token) * d.n_heads + head;
+        for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            __syncwarp();
+            if (n_kv > 0) {
+                tmem_ld16(tO + c, o);
+                tmem_wait_ld();
+                reg_fence16(o);
+            }
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = n_kv > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!live || c + 8 * half >= D) continue;
+                if (pl.parts == 1) {
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(d.out) + token * d.out_stride + head * D + c + 8 * half) =
+                        Vec<T>::pack(v + 8 * half);
+                } else {
+                    float4 *p = reinterpret_cast<float4 *>(pl.part_o + prow * D + c + 8 * half);
+                    p[0] = make_float4(v[8 * half], v[8 * half + 1], v[8 * half + 2], v[8 * half + 3]);
+                    p[1] = make_float4(v[8 * half + 4], v[8 * half + 5], v[8 * half + 6], v[8 * half + 7]);
+                }
+            }
+        }
+        if (live) {
+            if (pl.parts > 1) {
+                pl.part_lse[prow] = lse2;
+            } else if (d.lse) {
+                d.lse[token * d.n_heads + head] = lse2 * kLn2;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) __nanosleep(200000);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace vitk
+
+namespace vith {
+
+namespace {
+
+int key_map(CUtensorMap *m, const prefix_attention_desc &d, const void *p, int64_t token, int64_t head, int64_t seq,
+            int64_t len, int64_t n_seq) {
+    const uint64_t dims[4] = {static_cast<uint64_t>(d.head_dim), static_cast<uint64_t>(d.n_kv_heads),
+                              static_cast<uint64_t>(len), static_cast<uint64_t>(n_seq)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(head) * 2, static_cast<uint64_t>(token) * 2,
+                                 static_cast<uint64_t>(seq) * 2};
+    const uint32_t box[4] = {64, 1, kTcKeys, 1};
+    return tmap_nd(m, p, d.dtype == VIT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename T, int HV>
+cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(vitk::prefix_tc_kernel<T, HV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 vitk::kTcSmem<HV>);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    vitk::prefix_tc_kernel<T, HV><<<static_cast<unsigned>(items), vitk::kTcThreads, vitk::kTcSmem<HV>, s>>>(
+        m[0], m[1], m[2], m[3], a, kind);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s) {
+    if (items <= 0) return VIT_OK;
+    const prefix_attention_desc &d = a.d;
+    CUtensorMap m[4];
+    int rc = VIT_OK;
+    if (d.prefix_len > 0) {
+        rc = key_map(m, d, d.prefix_k, d.prefix_k_token, d.prefix_k_head, d.prefix_k_token, d.prefix_len, 1);
+        if (rc == VIT_OK) rc = key_map(m + 1, d, d.prefix_v, d.prefix_v_token, d.prefix_v_head, d.prefix_v_token, d.prefix_len, 1);
+    }
+    const bool own = d.k != nullptr && d.max_len > 0;
+    if (rc == VIT_OK && own) {
+        rc = key_map(m + 2, d, d.k, d.k_token, d.k_head, d.k_seq, d.max_len, d.n_seq);
+        if (rc == VIT_OK) rc = key_map(m + 3, d, d.v, d.v_token, d.v_head, d.v_seq, d.max_len, d.n_seq);
+    }
+    if (rc != VIT_OK) return rc;
+    if (d.prefix_len == 0 && own) {          // a map no item reads still has to be one
+        m[0] = m[2];
+        m[1] = m[3];
+    } else if (!own) {
+        m[2] = m[0];
+        m[3] = m[1];
+    }
+    cudaError_t e;
+    if (d.dtype == VIT_DTYPE_BF16)
+        e = d.head_dim <= 64 ? launch<__nv_bfloat16, 1>(m, a, kind, items, s) : launch<__nv_bfloat16, 2>(m, a, kind, items, s);
+    else
+        e = d.head_dim <= 64 ? launch<__half, 1>(m, a, kind, items, s) : launch<__half, 2>(m, a, kind, items, s);
+    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+}
+
+}  // namespace vith

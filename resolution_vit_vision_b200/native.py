@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Dict, Optional, Sequence
 
@@ -456,7 +457,9 @@ def scatter_vision_tokens(input_ids, embed_table, vision, out=None, status=None,
 
 
 # ------------------------------------------------------------------------------------------------
-# decoder-side steps with their gradients, and attention over a shared prefix (include/vit_decoder.h)
+# decoder-side steps with their gradients, and attention over a shared prefix (include/vit_decoder.h).
+# Decoding calls them once per layer and token with kernels of a few microseconds, so the marshalling
+# below reads each tensor property once and allocates with new_empty / empty_like.
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _HERE_AND_NOW = contextlib.nullcontext()
 
@@ -466,67 +469,86 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _place(t: torch.Tensor, stream):
-    """The context a call on ``t`` runs in: t's device current and, where a stream is given, that
-    stream current, so that outputs and workspaces made inside belong to it."""
-    if stream is not None:
-        _need(stream.device == t.device, "the stream belongs to another device than the tensors")
-        return torch.cuda.stream(stream)
-    return _HERE_AND_NOW if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
-
-
-def _same_device(*tensors) -> None:
+def _device_of(*tensors) -> int:
+    """The index of the GPU that holds all the tensors (None is skipped)."""
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        _need(t.is_cuda, "tensors must be on a GPU")
-        _need(dev is None or t.device == dev, "tensors are on different devices")
-        dev = t.device
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                _need(dev is None, "tensors are on different devices")
+                _need(i >= 0, "tensors must be on a GPU")
+                dev = i
+    return dev
+
+
+def _place(dev: int, stream):
+    """The context a call on GPU ``dev`` runs in: that GPU current and, where a stream is given, that
+    stream current, so that outputs and workspaces made inside belong to it."""
+    if stream is not None:
+        _need(stream.device.index == dev, "the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    return _HERE_AND_NOW if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+# the current stream's handle without making a torch.cuda.Stream of it (3 us), where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: _stream(None))
 
 
 def _heads_arg(x, what: str):
     """[L, heads, head_dim] with heads contiguous -> (pointer, token stride, heads)."""
     if x is None:
         return None, 0, 0
-    _need(x.dim() == 3, f"{what} must be [L, heads, head_dim]")
     L, H, D = x.shape
     st = x.stride()
-    _need((st[2] == 1 or D == 1) and (st[1] == D or H == 1), f"{what}: the heads of a token must be contiguous")
+    if not ((st[1] == D or H == 1) and (st[2] == 1 or D == 1)):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
     return x.data_ptr(), (st[0] if L > 1 else H * D), H
+
+
+def _key_strides(t):
+    """Strides of [..., tokens, heads, head_dim] in elements; those of dimensions of one element, which
+    torch leaves arbitrary, become head_dim."""
+    return tuple(t.shape[-1] if n == 1 else s for n, s in zip(t.shape, t.stride()))
 
 
 def _like(x, out, what: str):
     """``out``, or a new contiguous tensor like x (None for None)."""
-    if x is None:
-        _need(out is None, f"{what} given without its input")
-        return None
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _need(out.shape == x.shape and out.dtype == x.dtype, f"{what} must have its input's shape and type")
+        return None if x is None else x.new_empty(x.shape)
+    _need(x is not None, f"{what} given without its input")
+    _need(out.shape == x.shape and out.dtype == x.dtype and out.get_device() == x.get_device(),
+          f"{what} must have its input's shape, type and device")
     return out
 
 
 def _status_arg(status):
-    if status is not None:
-        _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32 [1]")
-    return _ptr(status)
+    if status is None:
+        return None
+    _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32 [1]")
+    return status.data_ptr()
 
 
-def _norm_args(q, k, pos, q_weight, k_weight, sections):
-    x = q if q is not None else k
-    _need(x is not None, "q or k must be given")
-    _need(q is None or k is None or (q.shape[0] == k.shape[0] and q.shape[2] == k.shape[2] and q.dtype == k.dtype),
-          "q and k must have the same tokens, head_dim and type")
-    _need(x.dtype in DTYPES, "q and k must be bf16, fp16 or fp32")
-    L, D = x.shape[0], x.shape[2]
+@functools.lru_cache(maxsize=64)
+def _sections_arg(sections):
+    return (ctypes.c_int32 * 3)(*sections)
+
+
+def _norm_args(q, k, pos, q_weight, k_weight):
+    x = k if q is None else q
+    _need(x is not None and x.dim() == 3, "q or k must be given, [L, heads, head_dim]")
+    L, _, D = x.shape
+    dt = DTYPES.get(x.dtype)
+    _need(dt is not None, "q and k must be bf16, fp16 or fp32")
+    if k is not None and k is not x:
+        _need(k.dim() == 3 and k.shape[0] == L and k.shape[2] == D and k.dtype == x.dtype,
+              "q and k must have the same tokens, head_dim and type")
     _need(pos.dtype == torch.int32 and pos.shape == (3, L) and pos.is_contiguous(), "pos must be contiguous int32 [3, L]")
     for w in (q_weight, k_weight):
-        _need(w is None or (w.dtype == x.dtype and w.shape == (D,) and w.is_contiguous()),
-              "weights must be [head_dim] of the type of q and k")
-    _same_device(q, k, pos, q_weight, k_weight)
-    sec = (ctypes.c_int32 * 3)(*(int(v) for v in sections))
-    return x, L, D, DTYPES[x.dtype], sec
+        if w is not None:
+            _need(w.dtype == x.dtype and w.shape == (D,) and w.is_contiguous(),
+                  "weights must be [head_dim] of the type of q and k")
+    return x, L, D, dt
 
 
 def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6, theta: float = MROPE_THETA,
@@ -535,16 +557,17 @@ def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6,
     pass (either may be None; token strides are free, so slices of a packed QKV product work); weights
     [head_dim] or None (ones); pos int32 [3, L]. Returns (q_out, k_out): new tensors, or the given
     ones, which may be q and k themselves."""
-    x, L, D, dt, sec = _norm_args(q, k, pos, q_weight, k_weight, sections)
-    with _place(x, stream):
+    x, L, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
+    dev = _device_of(q, k, pos, q_weight, k_weight)
+    with _place(dev, stream):
         q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
-        _same_device(x, q_out, k_out)
         qp, qs, H = _heads_arg(q, "q")
         kp, ks, Hk = _heads_arg(k, "k")
         qo, qos, _ = _heads_arg(q_out, "q_out")
         ko, kos, _ = _heads_arg(k_out, "k_out")
         check(lib().mrope_norm_apply(qp, qs, qo, qos, H, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight), _ptr(k_weight),
-                                     eps, _ptr(pos), L, theta, sec, _stream(None)), "mrope_norm_apply")
+                                     eps, pos.data_ptr(), L, theta, _sections_arg(tuple(sections)), _raw_stream(dev)),
+              "mrope_norm_apply")
     return q_out, k_out
 
 
@@ -553,19 +576,20 @@ def mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight=None, k_weight=None, eps
                     stream=None):
     """Gradient of ``mrope_norm_apply`` at the same q, k, weights and positions: (dq, dk, dq_weight,
     dk_weight), the weights' in fp32 (None with weight_grads False, or for a missing q or k)."""
-    x, L, D, dt, sec = _norm_args(q, k, pos, q_weight, k_weight, sections)
+    x, L, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
     for g, t in ((dq_out, q), (dk_out, k)):
         _need((g is None) == (t is None) and (g is None or (g.shape == t.shape and g.dtype == t.dtype)),
               "the outputs' gradients must have the shape and type of q and k")
-    with _place(x, stream):
+    dev = _device_of(q, k, pos, q_weight, k_weight, dq_out, dk_out)
+    with _place(dev, stream):
         dq, dk = _like(q, dq, "dq"), _like(k, dk, "dk")
-        _same_device(x, dq_out, dk_out, dq, dk)
-        dw = [None, None]
-        ws, ws_bytes = None, 0
+        dwq = dwk = ws = None
+        ws_bytes = 0
         if weight_grads:
-            dw = [None if t is None else torch.empty(D, dtype=torch.float32, device=x.device) for t in (q, k)]
             ws_bytes = lib().mrope_norm_grad_workspace(D)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+            ws = x.new_empty((ws_bytes,), dtype=torch.uint8)
+            dwq = None if q is None else x.new_empty((D,), dtype=torch.float32)
+            dwk = None if k is None else x.new_empty((D,), dtype=torch.float32)
         gq, gqs, _ = _heads_arg(dq_out, "dq_out")
         gk, gks, _ = _heads_arg(dk_out, "dk_out")
         qp, qs, H = _heads_arg(q, "q")
@@ -573,34 +597,41 @@ def mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight=None, k_weight=None, eps
         qo, qos, _ = _heads_arg(dq, "dq")
         ko, kos, _ = _heads_arg(dk, "dk")
         check(lib().mrope_norm_grad(gq, gqs, qp, qs, qo, qos, H, gk, gks, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight),
-                                    _ptr(k_weight), _ptr(dw[0]), _ptr(dw[1]), eps, _ptr(pos), L, theta, sec, _ptr(ws),
-                                    ws_bytes, _stream(None)), "mrope_norm_grad")
-    return dq, dk, dw[0], dw[1]
+                                    _ptr(k_weight), _ptr(dwq), _ptr(dwk), eps, pos.data_ptr(), L, theta,
+                                    _sections_arg(tuple(sections)), _ptr(ws), ws_bytes, _raw_stream(dev)),
+              "mrope_norm_grad")
+    return dq, dk, dwq, dwk
 
 
-def _ids_arg(input_ids):
+def _ids_arg(input_ids) -> int:
     _need(input_ids.dtype == torch.int32 and input_ids.dim() == 1 and input_ids.is_contiguous(),
           "input_ids must be contiguous int32 [L]")
+    return input_ids.shape[0]
 
 
 def embed_vision_tokens(input_ids, embed_table, vision=None, scale: float = 1.0, out=None, status=None, stream=None):
     """The decoder's input rows: scale * embedding for text ids, vision tokens (unscaled) at the image /
     video placeholders. bf16, fp16 or fp32, all of one type."""
-    _ids_arg(input_ids)
-    L, (V, D) = input_ids.shape[0], embed_table.shape
-    _need(embed_table.dtype in DTYPES and embed_table.is_contiguous(), "embed_table must be contiguous bf16, fp16 or fp32")
-    n_vis = 0 if vision is None else vision.shape[0]
-    _need(vision is None or (vision.dtype == embed_table.dtype and vision.shape == (n_vis, D) and vision.is_contiguous()),
-          "vision must be contiguous [n_vision, dim] of the table's type")
-    with _place(embed_table, stream):
+    L = _ids_arg(input_ids)
+    V, D = embed_table.shape
+    dtype = embed_table.dtype
+    dt = DTYPES.get(dtype)
+    _need(dt is not None and embed_table.is_contiguous(), "embed_table must be contiguous bf16, fp16 or fp32")
+    n_vis = 0
+    if vision is not None:
+        n_vis = vision.shape[0]
+        _need(vision.dtype == dtype and vision.shape == (n_vis, D) and vision.is_contiguous(),
+              "vision must be contiguous [n_vision, dim] of the table's type")
+    dev = _device_of(embed_table, input_ids, vision, out, status)
+    with _place(dev, stream):
         if out is None:
-            out = torch.empty((L, D), dtype=embed_table.dtype, device=embed_table.device)
-        _need(out.shape == (L, D) and out.dtype == embed_table.dtype and out.is_contiguous(),
-              "out must be contiguous [L, dim] of the table's type")
-        _same_device(input_ids, embed_table, vision, out, status)
-        check(lib().embed_vision_tokens(_ptr(input_ids), L, _ptr(embed_table), DTYPES[embed_table.dtype], V, D, scale,
-                                        _ptr(vision) if n_vis else None, n_vis, _ptr(out), _status_arg(status),
-                                        _stream(None)), "embed_vision_tokens")
+            out = embed_table.new_empty((L, D))
+        else:
+            _need(out.shape == (L, D) and out.dtype == dtype and out.is_contiguous(),
+                  "out must be contiguous [L, dim] of the table's type")
+        check(lib().embed_vision_tokens(input_ids.data_ptr(), L, embed_table.data_ptr(), dt, V, D, scale,
+                                        vision.data_ptr() if n_vis else None, n_vis, out.data_ptr(),
+                                        _status_arg(status), _raw_stream(dev)), "embed_vision_tokens")
     return out
 
 
@@ -609,32 +640,34 @@ def embed_vision_tokens_grad(input_ids, d_out, vocab: int, n_vision: int = 0, sc
     """Gradient of ``embed_vision_tokens``: (d_table [vocab, dim], d_vision [n_vision, dim] or None). d_table
     is of table_dtype (d_out's type, or fp32); a given d_table is overwritten, or added to with
     accumulate (then only the rows that input_ids names are touched)."""
-    _ids_arg(input_ids)
-    L = input_ids.shape[0]
-    _need(d_out.dtype in DTYPES and d_out.dim() == 2 and d_out.shape[0] == L and d_out.is_contiguous(),
+    L = _ids_arg(input_ids)
+    dtype = d_out.dtype
+    dt = DTYPES.get(dtype)
+    _need(dt is not None and d_out.dim() == 2 and d_out.shape[0] == L and d_out.is_contiguous(),
           "d_out must be contiguous [L, dim] in bf16, fp16 or fp32")
     D = d_out.shape[1]
     _need(d_table is not None or not accumulate, "accumulate needs a d_table to add to")
     if table_dtype is None:
-        table_dtype = d_out.dtype if d_table is None else d_table.dtype
-    _need(table_dtype in (d_out.dtype, torch.float32), "the table's gradient is of d_out's type or fp32")
-    with _place(d_out, stream):
+        table_dtype = dtype if d_table is None else d_table.dtype
+    _need(table_dtype in (dtype, torch.float32), "the table's gradient is of d_out's type or fp32")
+    dev = _device_of(d_out, input_ids, d_table, d_vision, status)
+    with _place(dev, stream):
         if d_table is None:
-            d_table = torch.empty((vocab, D), dtype=table_dtype, device=d_out.device)
+            d_table = d_out.new_empty((vocab, D), dtype=table_dtype)
         _need(d_table.shape == (vocab, D) and d_table.dtype == table_dtype and d_table.is_contiguous(),
               "d_table must be contiguous [vocab, dim] of table_dtype")
         if d_vision is None and n_vision:
-            d_vision = torch.empty((n_vision, D), dtype=d_out.dtype, device=d_out.device)
-        _need(d_vision is None or (d_vision.shape == (n_vision, D) and d_vision.dtype == d_out.dtype
+            d_vision = d_out.new_empty((n_vision, D))
+        _need(d_vision is None or (d_vision.shape == (n_vision, D) and d_vision.dtype == dtype
                                    and d_vision.is_contiguous()),
               "d_vision must be contiguous [n_vision, dim] of d_out's type")
-        _same_device(input_ids, d_out, d_table, d_vision, status)
-        ws_bytes = lib().embed_vision_tokens_grad_workspace(L, vocab, D)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=d_out.device)
-        check(lib().embed_vision_tokens_grad(_ptr(input_ids), L, _ptr(d_out), DTYPES[d_out.dtype], vocab, D, scale,
-                                             _ptr(d_table), DTYPES[table_dtype], 1 if accumulate else 0,
-                                             _ptr(d_vision), n_vision, _ptr(ws), ws_bytes, _status_arg(status),
-                                             _stream(None)), "embed_vision_tokens_grad")
+        L_ = lib()
+        ws_bytes = L_.embed_vision_tokens_grad_workspace(L, vocab, D)
+        ws = d_out.new_empty((ws_bytes,), dtype=torch.uint8)
+        check(L_.embed_vision_tokens_grad(input_ids.data_ptr(), L, d_out.data_ptr(), dt, vocab, D, scale,
+                                          d_table.data_ptr(), DTYPES[table_dtype], 1 if accumulate else 0,
+                                          _ptr(d_vision), n_vision, ws.data_ptr(), ws_bytes, _status_arg(status),
+                                          _raw_stream(dev)), "embed_vision_tokens_grad")
     return d_table, d_vision
 
 
@@ -651,62 +684,71 @@ def prefix_attention(q, prefix_k=None, prefix_v=None, k=None, v=None, lens=None,
     of n sees its sequence's keys s <= lens - n + j. Returns (out, lse): out like q, lse fp32 [total_q, heads]."""
     _need(q.dim() == 3 and q.dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16 [total_q, heads, head_dim]")
     T, H, D = q.shape
+    dtype = q.dtype
     _need((prefix_k is None) == (prefix_v is None) and (k is None) == (v is None), "keys and values go together")
     _need(prefix_k is not None or k is not None, "a prefix or own keys must be given")
     _need((k is None) == (lens is None), "own keys need their lengths")
+    Lp = B = None
     Hk = (prefix_k if prefix_k is not None else k).shape[-2]
-    d = PrefixAttentionDesc()
+    pk_token = pk_head = pv_token = pv_head = k_seq = k_token = k_head = v_seq = v_token = v_head = 0
+    pk = pv = kp = vp = lp = None
     if prefix_k is not None:
         Lp = prefix_k.shape[0]
-        for t in (prefix_k, prefix_v):
-            _need(t.shape == (Lp, Hk, D) and t.dtype == q.dtype and (t.stride(2) == 1 or D == 1),
-                  "prefix keys and values must be [prefix_len, kv_heads, head_dim] of q's type, head_dim contiguous")
-        d.prefix_len = Lp
+        i0, i1 = prefix_k.stride(2), prefix_v.stride(2)
+        _need(prefix_k.shape == (Lp, Hk, D) and prefix_v.shape == (Lp, Hk, D) and prefix_k.dtype == dtype
+              and prefix_v.dtype == dtype and ((i0 == 1 and i1 == 1) or D == 1),
+              "prefix keys and values must be [prefix_len, kv_heads, head_dim] of q's type, head_dim contiguous")
+        pk_token, pk_head, _ = _key_strides(prefix_k)
+        pv_token, pv_head, _ = _key_strides(prefix_v)
         if Lp:
-            d.prefix_k, d.prefix_v = prefix_k.data_ptr(), prefix_v.data_ptr()
-            (d.prefix_k_token, d.prefix_k_head, _), (d.prefix_v_token, d.prefix_v_head, _) = prefix_k.stride(), prefix_v.stride()
+            pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
     if k is not None:
         B, cap = k.shape[0], k.shape[1]
-        for t in (k, v):
-            _need(t.shape == (B, cap, Hk, D) and t.dtype == q.dtype and (t.stride(3) == 1 or D == 1),
-                  "own keys and values must be [n_seq, capacity, kv_heads, head_dim] of q's type, head_dim contiguous")
+        i0, i1 = k.stride(3), v.stride(3)
+        _need(k.shape == (B, cap, Hk, D) and v.shape == (B, cap, Hk, D) and k.dtype == dtype and v.dtype == dtype
+              and ((i0 == 1 and i1 == 1) or D == 1),
+              "own keys and values must be [n_seq, capacity, kv_heads, head_dim] of q's type, head_dim contiguous")
         _need(lens.dtype == torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [n_seq]")
         max_len = cap if max_len is None else max_len
         _need(0 <= max_len <= cap, "max_len must be within the capacity")
+        k_seq, k_token, k_head, _ = _key_strides(k)
+        v_seq, v_token, v_head, _ = _key_strides(v)
         if cap:
-            d.k, d.v, d.lens, d.max_len = k.data_ptr(), v.data_ptr(), lens.data_ptr(), max_len
-            (d.k_seq, d.k_token, d.k_head, _), (d.v_seq, d.v_token, d.v_head, _) = k.stride(), v.stride()
+            kp, vp, lp = k.data_ptr(), v.data_ptr(), lens.data_ptr()
     if cu_q is not None:
         _need(cu_q.dtype == torch.int32 and cu_q.dim() == 1 and cu_q.shape[0] >= 2 and cu_q.is_contiguous(),
               "cu_q must be int32 [n_seq + 1]")
         n_seq = cu_q.shape[0] - 1
         max_q = max(T, 1) if max_q is None else max_q
-        d.cu_q = cu_q.data_ptr()
     else:
         max_q = 1 if max_q is None else max_q
-        n_seq = k.shape[0] if k is not None else T // max(max_q, 1)
+        n_seq = B if B is not None else T // max(max_q, 1)
         _need(n_seq * max_q == T or T == 0, "without cu_q there must be max_q queries for each sequence")
-    _need(k is None or k.shape[0] == n_seq, "k and cu_q disagree on the number of sequences")
-    with _place(q, stream):
+    _need(B is None or B == n_seq, "k and cu_q disagree on the number of sequences")
+    dev = _device_of(q, prefix_k, prefix_v, k, v, lens, cu_q, out, lse, status)
+    with _place(dev, stream):
         if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+            out = q.new_empty((T, H, D))
+        else:
+            _need(out.shape == q.shape and out.dtype == dtype, "out must have q's shape and type")
         if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-        _need(out.shape == q.shape and out.dtype == q.dtype, "out must have q's shape and type")
-        _need(lse.shape == (T, H) and lse.dtype == torch.float32 and lse.is_contiguous(), "lse must be fp32 [total_q, heads]")
-        _same_device(q, prefix_k, prefix_v, k, v, lens, cu_q, out, lse, status)
+            lse = q.new_empty((T, H), dtype=torch.float32)
+        else:
+            _need(lse.shape == (T, H) and lse.dtype == torch.float32 and lse.is_contiguous(),
+                  "lse must be fp32 [total_q, heads]")
         if T == 0:
             return out, lse
-        d.dtype, d.n_heads, d.n_kv_heads, d.head_dim = DTYPES[q.dtype], H, Hk, D
-        d.scale, d.causal = (D ** -0.5 if scale is None else scale), 1 if causal else 0
-        d.q, d.q_stride, _ = _heads_arg(q, "q")
-        d.out, d.out_stride, _ = _heads_arg(out, "out")
-        d.lse, d.total_q, d.max_q, d.n_seq = lse.data_ptr(), T, max_q, n_seq
+        qp, qs, _ = _heads_arg(q, "q")
+        op, os_, _ = _heads_arg(out, "out")
+        d = PrefixAttentionDesc(DTYPES[dtype], H, Hk, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, qp, qs,
+                                op, os_, lse.data_ptr(), T, max_q, _ptr(cu_q), n_seq, pk, pv, Lp or 0, pk_token, pk_head,
+                                pv_token, pv_head, kp, vp, k_seq, k_token, k_head, v_seq, v_token, v_head, lp,
+                                max_len if kp is not None else 0)
         L = lib()
-        ws_bytes = L.prefix_attention_workspace(ctypes.byref(d))
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
-        check(L.prefix_attention(ctypes.byref(d), _ptr(ws), ws_bytes, _status_arg(status), _stream(None)),
-              "prefix_attention")
+        ref = ctypes.byref(d)
+        ws_bytes = L.prefix_attention_workspace(ref)
+        ws = q.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
+        check(L.prefix_attention(ref, _ptr(ws), ws_bytes, _status_arg(status), _raw_stream(dev)), "prefix_attention")
     return out, lse
 
 

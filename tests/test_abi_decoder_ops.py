@@ -126,7 +126,7 @@ def test_prefix_attention_refusals(nv, bad, code):
 
 
 def test_prefix_attention_workspace_is_checked(nv):
-    d = _desc(nv)
+    d = _desc(nv, n_seq=100, total_q=200, prefix_len=5000)     # long enough for parts
     need = nv.lib().prefix_attention_workspace(ctypes.byref(d))
     assert need > 0
     assert nv.lib().prefix_attention(ctypes.byref(d), None, 0, None, None) == nv.VIT_ERR_ARG

@@ -270,3 +270,31 @@ def test_decoder_step_end_to_end():
         assert np.abs(_np(out[b * n:(b + 1) * n]) - ref).max() <= 0.16 * vmax
         same, _ = oo.prefix_attention(_np(q)[at][P:], None, None, _np(k)[at][None], rv[at][None], [P + n], [0, n], D ** -0.5)
         assert np.abs(_np(out[b * n:(b + 1) * n]) - same).max() <= (2 * 2.0 ** -8 + 4e-4) * vmax
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("H, Hk, D", [(28, 4, 128), (8, 8, 64), (10, 2, 80), (3, 1, 24), (6, 2, 104)])
+@pytest.mark.parametrize("B, n_q, Lp", [(40, 1, 700), (9, 31, 333), (3, 100, 161)])
+def test_many_rows(B, n_q, Lp, H, Hk, D, t):
+    # enough rows for the tensor-core tiles: stacked decoding, and sequences of their own
+    lens = [n_q + (13 * b) % 90 for b in range(B)]
+    a, cu = _case(30, B, n_q, lens, Lp, H, Hk, D, t, cap=n_q + 95)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    _check(a, cu, nv.prefix_attention(**a, status=st))
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("n_q, lens", [([256, 1, 257], [256, 400, 257]), ([129], [300]), ([65, 200, 1, 0], [65, 200, 79, 80])])
+def test_long_questions_of_single_heads(n_q, lens):
+    a, cu = _case(31, len(n_q), n_q, lens, 0, 2, 2, 64, "bf16", cap=max(lens) + 1)
+    _check(a, cu, nv.prefix_attention(**a))
+    a, cu = _case(32, len(n_q), n_q, lens, 81, 2, 2, 128, "fp16", cap=max(lens) + 1)
+    _check(a, cu, nv.prefix_attention(**a, causal=False), causal=False)
+
+
+def test_dimensions_of_one_element_have_any_stride():
+    a, cu = _case(33, 1, 1, [1], 1, 4, 1, 64, "bf16")
+    want = nv.prefix_attention(**a)
+    b = dict(a, prefix_k=a["prefix_k"].as_strided((1, 1, 64), (1, 3, 1)), k=a["k"].as_strided((1, 1, 1, 64), (0, 7, 1, 1)))
+    got = nv.prefix_attention(**b)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
