@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     const prefix_attention_desc &d = a.d;
     const PrefixPlan &pl = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warp index and TMEM base go through a shuffle: the compiler then keeps what is made of them
+    // (descriptors, barrier addresses) in uniform registers, where the products read their operands
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int D = d.head_dim, G = pl.G;
 
     // ---- the item (as prefix_small_kernel's)
@@ -121,6 +123,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int n_kv = t1 - t0;
     const int n_x = rows > kTcM ? 2 : 1;                  // query tiles with rows
 
+    // ---- Q rows of the softmax warps: in flight while barriers and tensor memory are set up. Lane r owns
+    // row r of its warp's 32 (its address, later its scores); lanes fetch a row's 16-byte words together.
+    constexpr int kWords = HV * 8, kRowsAtOnce = 32 / kWords, kLoads = 32 / kRowsAtOnce;
+    const int x = warp >= 3 ? (warp - 3) >> 2 : warp - 1;        // query tile of a softmax or issuing warp
+    const int quarter = warp & 3;                                // tensor-memory lanes 32 * quarter ..
+    const int R = row0 + x * kTcM + quarter * 32 + lane;         // (softmax warps) row of the item's run
+    const int j = R / G, head = h * G + (R - j * G);
+    const int64_t token = q0 + j;
+    const bool live_row = warp >= 3 && R < row0 + rows;
+    uint4 qw[kLoads];
+    if (warp >= 3) {
+        const uint64_t at = live_row ? reinterpret_cast<uint64_t>(static_cast<const T *>(d.q) + token * d.q_stride + head * D) : 0;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const uint64_t p = __shfl_sync(0xffffffffu, at, u * kRowsAtOnce + lane / kWords);
+            qw[u] = make_uint4(0, 0, 0, 0);
+            if (p != 0 && lane % kWords * 8 < D) qw[u] = reinterpret_cast<const uint4 *>(p)[lane % kWords];
+        }
+    }
+
+    if (warp == 0 && lane < 4) {                          // the descriptors of the first loads
+        tma_prefetch(lane == 0 ? &tpk : lane == 1 ? &tpv : lane == 2 ? &tk : &tv);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kTcStages; ++s) {
             mbar_init(k_full + s, 1);
@@ -144,7 +169,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const WaitCtx wc{abort_flag, a.status};
     auto tile_key = [&](int t) { return (t < n_prefix_tiles ? t : t - n_prefix_tiles) * kTcNK; };
 
@@ -163,28 +188,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else if (warp == 1 || warp == 2) {
-        const int x = warp - 1;
         if (x < n_x && n_kv > 0) {
             const int ks = (D + 15) / 16;                 // 16-column steps of the head
             const uint32_t idS = idesc_f16(MmaType<T>::kCode, kTcM, kTcNK, false);
             const uint32_t idO = idesc_f16(MmaType<T>::kCode, kTcM, ks * 16, true);
             const uint32_t qa = smem_u32(sQ) + x * kQTile, ka = smem_u32(sK), va = smem_u32(sV);
+            // descriptors of the first step; later steps add constants (in units of 16 bytes)
+            const uint64_t dq = smem_desc(qa, 16, 1024, kSwizzle128B), dk = smem_desc(ka, 16, 1024, kSwizzle128B),
+                           dv = smem_desc(va, kTcKBox, 1024, kSwizzle128B);
             auto issue_s = [&](int i) {                   // S_x = Q_x K^T
                 const int st = i % kTcStages;
-                for (int c = 0; c < ks; ++c) {
-                    const uint32_t at = (c & 3) * 32;
-                    mma_bf16_ss(tmem + tc_s(x), smem_desc(qa + (c >> 2) * kTcQBox + at, 16, 1024, kSwizzle128B),
-                                smem_desc(ka + st * kTile + (c >> 2) * kTcKBox + at, 16, 1024, kSwizzle128B), idS,
-                                c > 0 ? 1u : 0u);
-                }
+                const uint64_t dks = dk + static_cast<uint32_t>(st * (kTile >> 4));
+#pragma unroll
+                for (int c = 0; c < HV * 4; ++c)
+                    if (c < ks)
+                        mma_bf16_ss(tmem + tc_s(x), dq + (((c >> 2) * kTcQBox + (c & 3) * 32) >> 4),
+                                    dks + (((c >> 2) * kTcKBox + (c & 3) * 32) >> 4), idS, c > 0 ? 1u : 0u);
                 mma_commit(s_full + x);
             };
             auto issue_pv = [&](int i) {                  // O_x += P_x V
                 const int st = i % kTcStages;
+                const uint64_t dvs = dv + static_cast<uint32_t>(st * (kTile >> 4));
 #pragma unroll
                 for (int kk = 0; kk < kTcNK / 16; ++kk)
-                    mma_bf16_ts(tmem + tc_o(x), tmem + tc_p(x) + kk * 8,
-                                smem_desc(va + st * kTile + kk * 2048, kTcKBox, 1024, kSwizzle128B), idO,
+                    mma_bf16_ts(tmem + tc_o(x), tmem + tc_p(x) + kk * 8, dvs + (kk * 2048 >> 4), idO,
                                 (i > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(o_done + x);
                 mma_commit(kv_empty + st);
@@ -193,7 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bool ok = mbar_wait(q_full + x, 0, wc) && wait_k(0);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            if (ok && lane == 0) issue_s(0);
+            if (ok && elect_one()) issue_s(0);
             for (int i = 0; ok && i < n_kv; ++i) {
                 const int st = i % kTcStages;
                 if (i + 1 < n_kv) {
@@ -201,7 +228,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) issue_s(i + 1);
+                    if (elect_one()) issue_s(i + 1);
                 }
                 ok = mbar_wait(v_full + st, (i / kTcStages) & 1, wc);
                 const int t = t0 + i, valid = t < n_prefix_tiles ? kTcNK : own_keys - tile_key(t);
@@ -217,38 +244,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) issue_pv(i);
+                if (elect_one()) issue_pv(i);
                 __syncwarp();
             }
         }
     } else if (warp < 3 + 4 * n_x) {
-        const int x = (warp - 3) >> 2;
-        const int quarter = warp & 3;
-        const int r = quarter * 32 + lane;                // row inside the tile
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + tc_s(x) + lane_off, tP = tmem + tc_p(x) + lane_off, tO = tmem + tc_o(x) + lane_off;
-        const T *q = static_cast<const T *>(d.q);
-        {   // Q rows into the swizzled layout of the products: 16-byte word c of row i goes to c ^ (i & 7)
-            constexpr int kWords = HV * 8, kRowsAtOnce = 32 / kWords;
-            const int c = lane % kWords;
-#pragma unroll 8
-            for (int i0 = 0; i0 < 32; i0 += kRowsAtOnce) {
-                const int i = quarter * 32 + i0 + lane / kWords, row = x * kTcM + i;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row < rows && c * 8 < D) {
-                    const int R = row0 + row;
-                    v = *reinterpret_cast<const uint4 *>(q + (q0 + R / G) * d.q_stride + (h * G + R % G) * D + c * 8);
-                }
-                *reinterpret_cast<uint4 *>(sQ + x * kQTile + (c >> 3) * kTcQBox + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(q_full + x);
+        uint8_t *const q_rows = sQ + x * kQTile + quarter * 32 * 128;   // this warp's rows of the tile's first half
+        // the swizzled layout of the products: 16-byte word c of row i goes to c ^ (i & 7)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int i = u * kRowsAtOnce + lane / kWords, c = lane % kWords;
+            *reinterpret_cast<uint4 *>(q_rows + (c >> 3) * kTcQBox + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = qw[u];
         }
-        const int R = row0 + x * kTcM + r;
-        const int j = R / G;
+        fence_proxy_async_smem();
+        mbar_arrive(q_full + x);
         const int lim = kind == 0 ? 0 : (d.causal ? min(len, len - n_q + j + 1) : len);
+        const int prefix_len = static_cast<int>(d.prefix_len);
         const float scale_log2 = d.scale * kLog2e;
-        float m_used = -INFINITY, l = 0.f;
+        float m_used = -INFINITY;
+        float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // the row's sum in eight shares
         bool ok = true;
         // the two groups take turns at the exponentials (named barriers 2 and 3), so one group's loads,
         // maxima and stores run while the other keeps the MUFU busy; B opens A's first turn
@@ -269,8 +285,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             reg_fence16(sr + 64);
             tc_fence_before();
             mbar_arrive(s_free + x);
-            const int t = t0 + i, k0 = tile_key(t);
-            const int valid = t < n_prefix_tiles ? static_cast<int>(min(static_cast<int64_t>(kTcNK), d.prefix_len - k0)) : lim - k0;
+            const int valid = t0 + i < n_prefix_tiles ? prefix_len - (t0 + i) * kTcNK : lim - (t0 + i - n_prefix_tiles) * kTcNK;
             if (__any_sync(0xffffffffu, valid < kTcNK)) {
 #pragma unroll
                 for (int k = 0; k < kTcNK; ++k)
@@ -289,10 +304,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                    fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale_log2;
             const bool need = mx > m_used + kTcRescale;
             const float alpha = (i > 0 && need) ? exp2_mufu(m_used - mx) : 1.0f;
-            l *= alpha;
-            if (need) m_used = mx;
+            if (need) {
+                m_used = mx;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) l8[e] *= alpha;
+            }
             const float neg_m = m_used == -INFINITY ? 0.f : -m_used;   // no visible key yet: every p stays 0
-            float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             uint32_t pk[kTcNK / 2];
             if (n_x == 2) named_bar_sync(my_turn, 256);
 #pragma unroll
@@ -304,12 +321,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int e = 0; e < 8; ++e) p[e] = exp2_mufu(p[e]);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    r8[(e >> 1) + 4 * ((k >> 3) & 1)] += p[e] + p[e + 1];
+                    l8[(e >> 1) + 4 * ((k >> 3) & 1)] += p[e] + p[e + 1];
                     pk[(k + e) >> 1] = pack2(p[e], p[e + 1], T());
                 }
             }
             if (n_x == 2 && (x == 0 || i + 1 < n_kv)) named_bar_arrive(their_turn, 256);
-            l += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
             // P_x V of the tile before must be complete before O_x is scaled or P_x overwritten
             if (i > 0) {
                 if (!mbar_wait(o_done + x, (i - 1) & 1, wc)) ok = false;
@@ -333,38 +349,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_before();
             mbar_arrive(p_full + x);
         }
+        const float l = ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
         if (n_kv > 0) ok = mbar_wait(o_done + x, (n_kv - 1) & 1, wc) && ok;
         tc_fence_after();
-        const int64_t token = q0 + j;
-        const int head = h * G + R % G;
-        bool live = ok && R < row0 + rows;
+        bool live = ok && live_row;
         if (kind == 0 && pl.parts == 1 && d.cu_q != nullptr) live = live && token < d.cu_q[d.n_seq];
         const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
         const float lse2 = (m_used == -INFINITY ? 0.f : m_used) + log2f(l);
         const int64_t prow = (static_cast<int64_t>(part) * d.total_q + token) * d.n_heads + head;
-        for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            __syncwarp();
-            if (n_kv > 0) {
-                tmem_ld16(tO + c, o);
-                tmem_wait_ld();
-                reg_fence16(o);
-            }
-            float v[16];
+        // o through shared memory (this warp's Q rows, no longer read), so that a row leaves in whole
+        // 128-byte lines: columns in two rounds of kCols, lane = row on the way in, lanes = words of a row
+        // on the way out
+        const bool whole = pl.parts == 1;
+        const int cols = whole ? HV * 64 : HV * 32;                 // columns per round: 16-byte words of T or float
+        const uint64_t to = !live ? 0
+                            : whole ? reinterpret_cast<uint64_t>(static_cast<T *>(d.out) + token * d.out_stride + head * D)
+                                    : reinterpret_cast<uint64_t>(pl.part_o + prow * D);
+        for (int c0 = 0; c0 < D; c0 += cols) {
+            for (int c = 0; c < cols && c0 + c < D; c += 32) {
+                uint32_t o[32];
+                if (n_kv > 0) {
+                    tmem_ld32(tO + c0 + c, o);
+                    tmem_wait_ld();
+                    reg_fence32(o);
+                }
+                float v[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = n_kv > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+                for (int e = 0; e < 32; ++e) v[e] = n_kv > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+                auto put = [&](int w, const uint4 &u) {             // 16-byte word w of row `lane`
+                    *reinterpret_cast<uint4 *>(q_rows + (w >> 3) * kTcQBox + lane * 128 + (((w & 7) ^ (lane & 7)) << 4)) = u;
+                };
+                if (whole) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!live || c + 8 * half >= D) continue;
-                if (pl.parts == 1) {
-                    *reinterpret_cast<uint4 *>(static_cast<T *>(d.out) + token * d.out_stride + head * D + c + 8 * half) =
-                        Vec<T>::pack(v + 8 * half);
+                    for (int e = 0; e < 4; ++e) put((c >> 3) + e, Vec<T>::pack(v + 8 * e));
                 } else {
-                    float4 *p = reinterpret_cast<float4 *>(pl.part_o + prow * D + c + 8 * half);
-                    p[0] = make_float4(v[8 * half], v[8 * half + 1], v[8 * half + 2], v[8 * half + 3]);
-                    p[1] = make_float4(v[8 * half + 4], v[8 * half + 5], v[8 * half + 6], v[8 * half + 7]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) put((c >> 2) + e, Vec<float>::pack(v + 4 * e));
                 }
             }
+            __syncwarp();
+            const int words = min(cols, D - c0) / (whole ? 8 : 4), first = c0 / (whole ? 8 : 4), w = lane % kWords;
+            constexpr int kBatch = 8;                               // words read before the first is stored
+#pragma unroll 1
+            for (int u0 = 0; u0 < kLoads; u0 += kBatch) {
+                uint4 r[kBatch];
+                uint64_t p[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = (u0 + u) * kRowsAtOnce + lane / kWords;
+                    p[u] = __shfl_sync(0xffffffffu, to, i);
+                    r[u] = *reinterpret_cast<const uint4 *>(q_rows + (w >> 3) * kTcQBox + i * 128 + (((w & 7) ^ (i & 7)) << 4));
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (p[u] != 0 && w < words) reinterpret_cast<uint4 *>(p[u])[first + w] = r[u];
+            }
+            __syncwarp();
         }
         if (live) {
             if (pl.parts > 1) {
