@@ -11,12 +11,14 @@
 //                        contiguous share per CTA, one contiguous range per warp; placeholders and
 //                        ids outside the table get the keys vocab and vocab + 1 and end up behind the
 //                        text, so the k-th placeholder is entry n_text + k. The CTAs meet at the
-//                        cluster's hardware barrier, so nothing spins on memory.
+//                        cluster's hardware barrier, so nothing spins on memory. The other clusters of
+//                        the launch meanwhile write zeros to the first rows of the table, as many as
+//                        HBM takes while the sort runs: it costs no time of its own.
 //   embed_reduce_kernel  sorted entries in chunks of a fixed size: a chunk's CTA adds up the rows of
 //                        each run of equal ids and writes the runs that lie inside the chunk; runs
 //                        that cross a border leave fp32 partial rows. Other CTAs of the same launch
-//                        copy the placeholders' rows and write zeros to the rows no token named (a
-//                        bit per table row, set by the sort).
+//                        copy the placeholders' rows and write zeros to the rest of the rows that no
+//                        token named (a bit per table row, set by the sort).
 //   embed_join_kernel    adds the partial rows of each run that crosses chunks, in chunk order.
 //
 // Bound by HBM: d_out is read once and, unless accumulating, the whole table's gradient is written
@@ -30,9 +32,11 @@
 namespace vitk {
 
 constexpr int kSortThreads = 1024, kSortWarps = 32, kSortBits = 9, kSortBins = 1 << kSortBits;
-constexpr int kSortSmem = (kSortWarps + 1) * kSortBins * 4 + 64 * 4;
-constexpr int kSortOneCta = 4096;         // up to this many tokens one CTA sorts alone
 constexpr int kSortCluster = 8;
+constexpr int kSortHeld = 8;              // entries of a lane in registers at a time
+constexpr int kSortOneCta = 4096;         // up to this many tokens one CTA sorts alone, in shared memory
+template <int CTAS>
+constexpr int kSortSmem = (kSortWarps + 1) * kSortBins * 4 + 64 * 4 + (CTAS == 1 ? kSortOneCta * 8 : 0);
 
 struct EmbedWs {                          // device workspace of one call
     uint2 *a, *b;                         // (key, position) buffers, L each
@@ -48,46 +52,84 @@ __device__ __forceinline__ uint32_t embed_key(int id, int64_t vocab) {
     return id >= 0 && id < vocab ? static_cast<uint32_t>(id) : static_cast<uint32_t>(vocab) + 1u;
 }
 
+// lanes of the warp with the same digit (`in`: this lane has one), by a ballot per bit
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, bool in) {
+    uint32_t same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < kSortBits; ++b) {
+        const bool one = (d >> b) & 1u;
+        const uint32_t v = __ballot_sync(0xffffffffu, one);
+        same &= one ? v : ~v;
+    }
+    return same;
+}
+
+template <int CTAS>
 __global__ void __launch_bounds__(kSortThreads, 1)
-    embed_sort_kernel(const int32_t *__restrict__ ids, int L, int64_t vocab, int64_t n_vision, int passes, int ctas,
-                      bool mark, EmbedWs ws, int32_t *status) {
-    extern __shared__ uint32_t s_hist[];                       // [warps][bins], then [bins]
+    embed_sort_kernel(const int32_t *__restrict__ ids, int L, int64_t vocab, int64_t n_vision, int passes, bool mark,
+                      EmbedWs ws, uint4 *__restrict__ zeros, int64_t n_zeros, int32_t *status) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x >= CTAS) {                                  // not the sorting cluster: zeros
+        const int64_t stride = static_cast<int64_t>(gridDim.x - CTAS) * kSortThreads;
+#pragma unroll 4
+        for (int64_t i = static_cast<int64_t>(blockIdx.x - CTAS) * kSortThreads + tid; i < n_zeros; i += stride)
+            zeros[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    extern __shared__ __align__(16) uint32_t s_hist[];         // [warps][bins], then [bins]
     uint32_t *s_base = s_hist + kSortWarps * kSortBins;
     uint32_t *s_scan = s_base + kSortBins;                     // 32 warp sums
     int *s_cnt = reinterpret_cast<int *>(s_scan + 32);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint2 *s_x = reinterpret_cast<uint2 *>(s_scan + 64);       // one CTA: the entries between passes
     const int rank = blockIdx.x;                               // one cluster: rank in it
-    const int per_warp = ((L + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+    const int per_warp = ((L + CTAS * kSortWarps - 1) / (CTAS * kSortWarps) + 31) / 32 * 32;
     const int w0 = min(L, (rank * kSortWarps + warp) * per_warp), w1 = min(L, w0 + per_warp);
     uint32_t *hist = s_hist + warp * kSortBins;
     if (tid < 2) s_cnt[tid] = 0;
     if (mark)
-        for (int64_t i = static_cast<int64_t>(rank) * kSortThreads + tid; i < (vocab + 31) / 32; i += ctas * kSortThreads)
+        for (int64_t i = static_cast<int64_t>(rank) * kSortThreads + tid; i < (vocab + 31) / 32; i += CTAS * kSortThreads)
             ws.named[i] = 0;
     __syncthreads();
     const uint2 *src = ws.b;
     uint2 *dst = ws.a;
+    constexpr int kBlock = 32 * kSortHeld;                     // entries of a warp in registers at a time
+    const bool held = w1 - w0 <= kBlock;                       // all of them: read once per pass
+    uint2 e[kSortHeld];
+    uint32_t same[kSortHeld];
     for (int p = 0; p < passes; ++p) {
         const int shift = p * kSortBits;
-        auto entry = [&](int i) {
-            return p == 0 ? make_uint2(embed_key(ids[i], vocab), static_cast<uint32_t>(i))
-                          : __ldcg(src + i);
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < kSortHeld; ++k) {
+                const int i = i0 + 32 * k + lane;
+                e[k] = make_uint2(0u, 0u);
+                if (i < w1)
+                    e[k] = p == 0      ? make_uint2(static_cast<uint32_t>(ids[i]), static_cast<uint32_t>(i))
+                           : CTAS == 1 ? s_x[i]
+                                       : __ldcg(src + i);
+            }
+            if (p == 0)
+#pragma unroll
+                for (int k = 0; k < kSortHeld; ++k) e[k].x = embed_key(static_cast<int>(e[k].x), vocab);
         };
         for (int d = lane; d < kSortBins; d += 32) hist[d] = 0;
         __syncwarp();
         int n_text = 0, n_vis = 0;
-        for (int i0 = w0; i0 < w1; i0 += 32) {                 // digits of this warp's range
-            const int i = i0 + lane;
-            const bool in = i < w1;
-            const uint32_t key = in ? entry(i).x : 0u;
-            const uint32_t d = in ? (key >> shift) & (kSortBins - 1) : kSortBins + lane;
-            if (p == 0) {
-                n_text += in && key < vocab;
-                n_vis += in && key == vocab;
+        for (int i0 = w0; i0 < w1; i0 += kBlock) {             // digits of this warp's range
+            load(i0);
+#pragma unroll
+            for (int k = 0; k < kSortHeld; ++k) {
+                if (i0 + 32 * k >= w1) break;
+                const bool in = i0 + 32 * k + lane < w1;
+                const uint32_t d = (e[k].x >> shift) & (kSortBins - 1);
+                if (p == 0) {
+                    n_text += in && e[k].x < vocab;
+                    n_vis += in && e[k].x == vocab;
+                }
+                same[k] = same_digit(d, in);
+                if (in && (same[k] & ((1u << lane) - 1u)) == 0) hist[d] += __popc(same[k]);
+                __syncwarp();
             }
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            if (in && (same & ((1u << lane) - 1u)) == 0) hist[d] += __popc(same);
-            __syncwarp();
         }
         if (p == 0) {
             n_text = __reduce_add_sync(0xffffffffu, n_text);
@@ -99,28 +141,29 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         }
         __syncthreads();
         uint32_t *gh = ws.hist + (p & 1) * kSortCluster * kSortBins;
+        uint32_t all = 0, before = 0;
         if (tid < kSortBins) {                                 // exclusive over the warps; the CTA's total
-            uint32_t run = 0;
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
                 const uint32_t c = s_hist[w * kSortBins + tid];
-                s_hist[w * kSortBins + tid] = run;
-                run += c;
+                s_hist[w * kSortBins + tid] = all;
+                all += c;
             }
-            gh[rank * kSortBins + tid] = run;
+            if (CTAS > 1) gh[rank * kSortBins + tid] = all;
         }
-        if (p == 0 && tid < 2) ws.count[rank * 2 + tid] = s_cnt[tid];
-        if (ctas > 1) {
+        if (CTAS > 1) {
+            if (p == 0 && tid < 2) ws.count[rank * 2 + tid] = s_cnt[tid];
             cluster_sync();
-        } else {
-            __syncthreads();
         }
         if (tid < kSortBins) {                                 // first place of each digit for this CTA
-            uint32_t all = 0, before = 0;
-            for (int c = 0; c < ctas; ++c) {
-                const uint32_t h = __ldcg(gh + c * kSortBins + tid);
-                if (c < rank) before += h;
-                all += h;
+            if (CTAS > 1) {
+                all = 0;
+#pragma unroll
+                for (int c = 0; c < CTAS; ++c) {
+                    const uint32_t n = __ldcg(gh + c * kSortBins + tid);
+                    if (c < rank) before += n;
+                    all += n;
+                }
             }
             uint32_t inc = all;
 #pragma unroll
@@ -138,26 +181,35 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             s_base[tid] += add;
         }
         __syncthreads();
-        for (int d = lane; d < kSortBins; d += 32) hist[d] += s_base[d];
+#pragma unroll
+        for (int d = 0; d < kSortBins; d += 32) hist[d + lane] += s_base[d + lane];
         __syncwarp();
-        for (int i0 = w0; i0 < w1; i0 += 32) {                 // stable: ranks inside a warp by lane
-            const int i = i0 + lane;
-            const bool in = i < w1;
-            const uint2 e = in ? entry(i) : make_uint2(0u, 0u);
-            const uint32_t d = in ? (e.x >> shift) & (kSortBins - 1) : kSortBins + lane;
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            const uint32_t at = in ? hist[d] + __popc(same & ((1u << lane) - 1u)) : 0u;
-            __syncwarp();
-            if (in) {
-                dst[at] = e;
-                if ((same >> lane) == 1u) hist[d] = at + 1u;   // the last lane of each digit
-                if (p == 0 && mark && e.x < vocab) atomicOr(ws.named + (e.x >> 5), 1u << (e.x & 31));
+        const bool last = p == passes - 1;
+        for (int i0 = w0; i0 < w1; i0 += kBlock) {             // stable: ranks inside a warp by lane
+            if (!held) load(i0);
+#pragma unroll
+            for (int k = 0; k < kSortHeld; ++k) {
+                if (i0 + 32 * k >= w1) break;
+                const bool in = i0 + 32 * k + lane < w1;
+                const uint32_t d = (e[k].x >> shift) & (kSortBins - 1);
+                if (!held) same[k] = same_digit(d, in);
+                const uint32_t at = in ? hist[d] + __popc(same[k] & ((1u << lane) - 1u)) : 0u;
+                __syncwarp();
+                if (in) {
+                    if (CTAS == 1 && !last) {
+                        s_x[at] = e[k];
+                    } else {
+                        dst[at] = e[k];
+                    }
+                    if ((same[k] >> lane) == 1u) hist[d] = at + 1u;   // the last lane of each digit
+                    if (p == 0 && mark && e[k].x < vocab) atomicOr(ws.named + (e[k].x >> 5), 1u << (e[k].x & 31));
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         if (p == 0 && rank == 0 && tid == 0) {
-            int t = 0, v = 0;
-            for (int c = 0; c < ctas; ++c) {
+            int t = s_cnt[0], v = s_cnt[1];
+            for (int c = 1; c < CTAS; ++c) {
                 t += __ldcg(ws.count + 2 * c);
                 v += __ldcg(ws.count + 2 * c + 1);
             }
@@ -165,13 +217,15 @@ __global__ void __launch_bounds__(kSortThreads, 1)
             ws.head[1] = v;
             if (status && (v != n_vision || t + v != L)) atomicExch(status, VIT_ERR_TOKENS);
         }
-        if (ctas > 1) {
+        if (CTAS > 1) {
             cluster_sync();
         } else {
             __syncthreads();
         }
-        src = dst;
-        dst = dst == ws.a ? ws.b : ws.a;
+        if (CTAS > 1) {
+            src = dst;
+            dst = dst == ws.a ? ws.b : ws.a;
+        }
     }
 }
 
@@ -237,9 +291,24 @@ struct EmbedReduceArgs {
     int64_t vocab, n_vision;
     int dim, chunk, n_chunks, slabs;
     int sum_ctas, vision_ctas;
+    int64_t zero_from, zero_to;           // rows below are zeroed by the sort's launch, those behind by the join's
+    int join_ctas, join_cols;
     float scale;
     bool accumulate;
 };
+
+// zeros in the rows r0 .. r0 + 31 (up to `end`) that no token named, a warp per row
+template <typename G>
+__device__ __forceinline__ void zero_rows(const EmbedReduceArgs &a, int64_t r0, int64_t end) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t bits = a.named[r0 / 32];
+    const int vecs = a.dim * static_cast<int>(sizeof(G)) / 16;
+    for (int i = threadIdx.x >> 5; i < kZeroRows && r0 + i < end; i += blockDim.x / 32) {
+        if ((bits >> i) & 1u) continue;
+        uint4 *dst = static_cast<uint4 *>(a.d_table) + (r0 + i) * vecs;
+        for (int c = lane; c < vecs; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
+    }
+}
 
 template <typename T, typename G>
 __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const __grid_constant__ EmbedReduceArgs a) {
@@ -312,15 +381,8 @@ __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const __gr
             for (int u = 0; u < 8; ++u)
                 if (c + 32 * u < vecs) dst[c + 32 * u] = v[u];
         }
-    } else {                                                  // ---- rows no token named: zeros
-        const int64_t r0 = static_cast<int64_t>(blockIdx.x - a.sum_ctas - a.vision_ctas) * kZeroRows;
-        const uint32_t bits = a.named[r0 / 32];
-        const int vecs = a.dim * static_cast<int>(sizeof(G)) / 16;
-        for (int i = warp; i < kZeroRows && r0 + i < a.vocab; i += kReduceThreads / 32) {
-            if ((bits >> i) & 1u) continue;
-            uint4 *dst = static_cast<uint4 *>(a.d_table) + (r0 + i) * vecs;
-            for (int c = lane; c < vecs; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
-        }
+    } else {
+        zero_rows<G>(a, a.zero_from + static_cast<int64_t>(blockIdx.x - a.sum_ctas - a.vision_ctas) * kZeroRows, a.zero_to);
     }
 }
 static_assert(kZeroRows == 32, "one word of row bits per zero-writing CTA");
@@ -329,8 +391,12 @@ constexpr int kJoinThreads = 256, kJoinCols = 256, kJoinGroups = kJoinThreads / 
 
 template <typename G>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_constant__ EmbedReduceArgs a) {
+    if (blockIdx.x >= a.join_ctas) {
+        zero_rows<G>(a, a.zero_to + static_cast<int64_t>(blockIdx.x - a.join_ctas) * kZeroRows, a.vocab);
+        return;
+    }
     const int n_text = a.head[0];
-    const int chunk = blockIdx.x, c0 = chunk * a.chunk, c1 = c0 + a.chunk;
+    const int chunk = blockIdx.x / a.join_cols, col0 = blockIdx.x % a.join_cols * kJoinCols, c0 = chunk * a.chunk, c1 = c0 + a.chunk;
     if (c1 >= n_text) return;                                 // the last chunk ends its runs
     const uint32_t key = a.sorted[c1 - 1].x;
     if (a.sorted[c1].x != key) return;                        // no run leaves this chunk
@@ -347,7 +413,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_c
     const int last = (lo - 1) / a.chunk;                      // the chunk in which the run ends
     __shared__ float4 s[kJoinGroups][kJoinCols / 4];
     const int tc = threadIdx.x % (kJoinCols / 4), grp = threadIdx.x / (kJoinCols / 4);
-    const int col = blockIdx.y * kJoinCols + tc * 4;
+    const int col = col0 + tc * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < a.dim) {
         // partial 0 is the run's tail in its first chunk, partial i the head of chunk + i
@@ -364,7 +430,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_c
     s[grp][tc] = acc;
     __syncthreads();
     if (threadIdx.x < kJoinCols / 8) {
-        const int c8 = blockIdx.y * kJoinCols + threadIdx.x * 8;
+        const int c8 = col0 + threadIdx.x * 8;
         if (c8 < a.dim) {
             float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -422,28 +488,43 @@ size_t layout(char *base, int64_t L, int64_t vocab, int dim, vitk::EmbedWs *w) {
     return at;
 }
 
-bool configure_sort() {
+template <int CTAS>
+cudaError_t sort(const int32_t *ids, int64_t L, int64_t vocab, int64_t n_vision, int passes, bool mark,
+                 const vitk::EmbedWs &ws, void *zeros, int64_t n_zeros, int32_t *status, cudaStream_t s) {
     static bool configured[64] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (dev < 64 && configured[dev]) return true;
-    if (cudaFuncSetAttribute(vitk::embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, vitk::kSortSmem) !=
-        cudaSuccess)
-        return false;
-    if (dev < 64) configured[dev] = true;
-    return true;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(vitk::embed_sort_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 vitk::kSortSmem<CTAS>);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = true;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CTAS;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(n_zeros > 0 ? 144 + CTAS : CTAS);       // the zeros' CTAs fill the other SMs
+    cfg.blockDim = dim3(vitk::kSortThreads);
+    cfg.dynamicSmemBytes = vitk::kSortSmem<CTAS>;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, vitk::embed_sort_kernel<CTAS>, ids, static_cast<int>(L), vocab, n_vision, passes, mark,
+                              ws, static_cast<uint4 *>(zeros), n_zeros, status);
 }
 
 template <typename T, typename G>
 cudaError_t reduce(const vitk::EmbedReduceArgs &a, cudaStream_t s) {
-    const int64_t zero = a.accumulate ? 0 : (a.vocab + vitk::kZeroRows - 1) / vitk::kZeroRows;
-    const int64_t grid = a.sum_ctas + a.vision_ctas + zero;
+    const int64_t grid = a.sum_ctas + a.vision_ctas + (a.zero_to - a.zero_from + vitk::kZeroRows - 1) / vitk::kZeroRows;
     if (grid > 0)
         vitk::embed_reduce_kernel<T, G><<<static_cast<unsigned>(grid), vitk::kReduceThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.n_chunks > 1) {
-        vitk::embed_join_kernel<G><<<dim3(a.n_chunks - 1, (a.dim + vitk::kJoinCols - 1) / vitk::kJoinCols),
-                                     vitk::kJoinThreads, 0, s>>>(a);
+    const int64_t rest = a.accumulate ? 0 : (a.vocab - a.zero_to + vitk::kZeroRows - 1) / vitk::kZeroRows;
+    if (e == cudaSuccess && a.join_ctas + rest > 0) {
+        vitk::embed_join_kernel<G><<<static_cast<unsigned>(a.join_ctas + rest), vitk::kJoinThreads, 0, s>>>(a);
         e = cudaGetLastError();
     }
     return e;
@@ -458,29 +539,24 @@ int64_t embed_grad_workspace(int64_t L, int64_t vocab, int dim) {
 int embed_grad_launch(const int32_t *ids, int64_t L, const void *d_out, int dtype, int64_t vocab, int dim, float scale,
                       void *d_table, int table_dtype, bool accumulate, void *d_vision, int64_t n_vision, void *workspace,
                       int32_t *status, cudaStream_t s) {
-    if (!configure_sort()) return VIT_ERR_CUDA;
     vitk::EmbedWs ws;
     layout(static_cast<char *>(workspace), L, vocab, dim, &ws);
     int bits = 1;
     while (bits < 32 && (int64_t(1) << bits) < vocab + 2) ++bits;
     const int passes = (bits + vitk::kSortBits - 1) / vitk::kSortBits;
-    const int ctas = L <= vitk::kSortOneCta ? 1 : vitk::kSortCluster;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(vitk::kSortThreads);
-    cfg.dynamicSmemBytes = vitk::kSortSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, vitk::embed_sort_kernel, ids, static_cast<int>(L), vocab, n_vision, passes, ctas,
-                           !accumulate, ws, status) != cudaSuccess)
-        return VIT_ERR_CUDA;
+    const bool one = L <= vitk::kSortOneCta;
+    // rows zeroed beside the sort and beside the join: what HBM takes meanwhile (about 5 MB per us)
+    const double sort_us = one ? 6.0 + L / 450.0 : 12.0 + L / 2500.0, join_us = 6.0;
+    const int64_t row_bytes = int64_t(dim) * (table_dtype == VIT_DTYPE_F32 ? 4 : 2);
+    auto rows_in = [&](double us) { return static_cast<int64_t>(us * 5.0e6 / row_bytes) / 32 * 32; };
+    const int64_t zero_rows = accumulate ? 0 : std::min<int64_t>(vocab / 32 * 32, rows_in(sort_us));
+    const int64_t n_zeros = zero_rows * (row_bytes / 16);
+    cudaError_t e = one ? sort<1>(ids, L, vocab, n_vision, passes, !accumulate, ws, d_table, n_zeros, status, s)
+                        : sort<vitk::kSortCluster>(ids, L, vocab, n_vision, passes, !accumulate, ws, d_table, n_zeros,
+                                                   status, s);
+    if (e != cudaSuccess) return VIT_ERR_CUDA;
     vitk::EmbedReduceArgs a;
-    a.sorted = passes % 2 ? ws.a : ws.b;
+    a.sorted = one || passes % 2 ? ws.a : ws.b;
     a.head = ws.head;
     a.named = ws.named;
     a.part = ws.part;
@@ -497,7 +573,13 @@ int embed_grad_launch(const int32_t *ids, int64_t L, const void *d_out, int dtyp
     a.vision_ctas = static_cast<int>((n_vision + vitk::kReduceThreads / 32 - 1) / (vitk::kReduceThreads / 32));
     a.scale = scale;
     a.accumulate = accumulate;
-    cudaError_t e;
+    a.zero_from = zero_rows;
+    a.join_cols = (dim + vitk::kJoinCols - 1) / vitk::kJoinCols;
+    a.join_ctas = std::max(0, a.n_chunks - 1) * a.join_cols;
+    // the join's share: only beside a join, and behind the rows of the sort's launch
+    a.zero_to = accumulate ? zero_rows
+                : a.join_ctas == 0 ? vocab
+                                   : std::max(zero_rows, (vocab - std::min(vocab, rows_in(join_us))) / 32 * 32);
     if (dtype == VIT_DTYPE_F32)
         e = reduce<float, float>(a, s);
     else if (dtype == VIT_DTYPE_BF16)

@@ -9,24 +9,28 @@
 // Both sums of a head (x^2 and g x) are taken in one round of shuffles, since r factors out.
 //
 // Bound by HBM: the forward reads and writes every element once, the gradient reads x and dy and
-// writes dx. A lane owns one 16-byte vector of the lower half of a head and the matching one of the
-// upper half, so a head is D / (2 kVec) lanes (8 for 128 16-bit dims), its sums are shuffles inside
-// that group and a pair never leaves its lane. Heads whose lane count is not a power of two (D = 80,
-// 96) leave the group's last lanes idle. A CTA takes a tile of tokens; cos / sin and the weights sit
-// in shared memory in an order that gives the lanes of a group consecutive 16-byte words. All
-// arithmetic is fp32 (angles fp64), rounded once to the element type on the way out.
+// writes dx. A warp takes a token (or a share of its heads, when there are few tokens) by itself, with
+// no barriers: a lane owns one 16-byte vector of the lower half of a head and the matching one of the
+// upper half, a head is D / (2 kVec) lanes (8 for 128 16-bit dims), its sums are shuffles inside that
+// group, and as the lane's dims stay the same from head to head, cos, sin and weights are read once per
+// token into registers. Vectors arrive by cp.async in a ring of each thread's own, several heads (and
+// tokens) ahead, so bytes in flight do not cost registers: loads straight into registers kept 38 KB per
+// SM in flight and 4.7 TB/s. Heads whose lane count is not a power of two (D = 80, 96) leave the
+// group's last lanes idle. Arithmetic is fp32 in pairs (fma.rn.f32x2), angles fp64, rounded once to the
+// element type on the way out.
 #include <algorithm>
 #include <cmath>
 
 #include "dtype.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace vitk {
 
 constexpr int kNormMaxFreq = 128;       // head_dim <= 256
-constexpr int kNormThreads = 256;
-constexpr int kNormMaxTile = 8;         // tokens per tile
-constexpr int kNormGradCtas = 592;      // at most this many CTAs write partial weight gradients
+constexpr int kNormThreads = 128, kNormWarps = kNormThreads / 32;
+constexpr int kNormCtas = 148 * 6;      // persistent CTAs of the forward
+constexpr int kNormGradCtas = 148 * 4;  // of the gradient: also the partial rows of the weight gradients
 
 struct NormRopeArgs {
     const void *x[2];                   // q, k
@@ -39,58 +43,102 @@ struct NormRopeArgs {
     float eps;
     const int32_t *pos;
     int64_t L;
-    int tile;                           // tokens per tile
+    int share_log2;                     // warps per token: 1, 2 or 4
+    float inv_d;                        // 1 / D
     float *dw_part;                     // [grid][2][D], gradient only, may be null
     int n_freq, axis_end0, axis_end1;
-    double inv_freq[kNormMaxFreq];
+    double power[7];                    // theta^(-2 / D) to the powers 1, 2, 4, ..., 64
 };
 
-// Shared arrays hold element e of lane g at [e / 4][g][e % 4]: a group's lanes read consecutive
-// 16-byte words.
-template <int V>
-__device__ __forceinline__ int lane_slot(int j, int lanes) {   // j: dim inside a half
-    const int g = j / V, e = j % V;
-    return ((e >> 2) * lanes + g) * 4 + (e & 3);
+// two fp32 lanes of work in one 64-bit register
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_of(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
+__device__ __forceinline__ void f2_get(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    float a, b;
+    f2_get(v, a, b);
+    return a + b;
+}
+template <typename T>
+__device__ __forceinline__ void unpack_f2(const uint4 &v, f2 *o) {
+    float f[Vec<T>::kVec];
+    Vec<T>::unpack(v, f);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::kVec / 2; ++e) o[e] = f2_of(f[2 * e], f[2 * e + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_f2(const f2 *o) {
+    float f[Vec<T>::kVec];
+#pragma unroll
+    for (int e = 0; e < Vec<T>::kVec / 2; ++e) f2_get(o[e], f[2 * e], f[2 * e + 1]);
+    return Vec<T>::pack(f);
+}
+
+// A lane's V consecutive floats of a shared array, as pairs.
 template <int V>
-__device__ __forceinline__ void lane_read(const float *s, int g, int lanes, float *f) {
+__device__ __forceinline__ void lane_read(const float *s, int g, f2 *o) {
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) {
-        const float4 v = *reinterpret_cast<const float4 *>(s + (c * lanes + g) * 4);
-        f[4 * c] = v.x;
-        f[4 * c + 1] = v.y;
-        f[4 * c + 2] = v.z;
-        f[4 * c + 3] = v.w;
+        const float4 v = *reinterpret_cast<const float4 *>(s + g * V + 4 * c);
+        o[2 * c] = f2_of(v.x, v.y);
+        o[2 * c + 1] = f2_of(v.z, v.w);
     }
 }
 
-// cos and sin of a tile's angles: position x frequency formed and reduced modulo 2 pi in double
-// (positions reach 10^5, where an fp32 angle is off by 10^-2 rad), then fp32
-template <int V>
-__device__ __forceinline__ void tile_angles(const NormRopeArgs &a, int64_t l0, int tokens, float *s_cos, float *s_sin) {
-    const int lanes = a.D / (2 * V);
-    for (int i = threadIdx.x; i < tokens * a.n_freq; i += blockDim.x) {
-        const int tt = i / a.n_freq, j = i - tt * a.n_freq;
-        const int axis = j < a.axis_end0 ? 0 : (j < a.axis_end1 ? 1 : 2);
-        const double ang = static_cast<double>(a.pos[axis * a.L + l0 + tt]) * a.inv_freq[j];
-        const double r = ang - 6.283185307179586476925 * rint(ang * 0.159154943091895335768883763);
-        float sv, cv;
-        sincosf(static_cast<float>(r), &sv, &cv);
-        const int at = tt * a.n_freq + lane_slot<V>(j, lanes);
-        s_cos[at] = cv;
-        s_sin[at] = sv;
+// Frequencies a lane forms the angles of: j = lane, lane + 32, ..., in turns per position
+constexpr int kLaneFreqs = kNormMaxFreq / 32;
+struct LaneFreqs {
+    double f[kLaneFreqs];
+    __device__ __forceinline__ void load(const NormRopeArgs &a, int lane) {
+#pragma unroll
+        for (int k = 0; k < kLaneFreqs; ++k) {
+            const int j = lane + 32 * k;
+            if (32 * k >= a.n_freq) break;
+            f[k] = 0.159154943091895335768883763;
+#pragma unroll
+            for (int b = 0; b < 7; ++b)
+                if ((j >> b) & 1) f[k] *= a.power[b];
+        }
     }
-}
+    // cos and sin of the token's angles into the warp's shared arrays: position x frequency in whole
+    // turns, its fraction taken in double (positions reach 10^5, where an fp32 angle is off by 10^-2 rad)
+    __device__ __forceinline__ void angles(const NormRopeArgs &a, int64_t l, int lane, float *s_cos, float *s_sin) const {
+        const int p0 = a.pos[l], p1 = a.pos[a.L + l], p2 = a.pos[2 * a.L + l];
+        __syncwarp();                    // the warp has read the token before's
+#pragma unroll
+        for (int k = 0; k < kLaneFreqs; ++k) {
+            const int j = lane + 32 * k;
+            if (j >= a.n_freq) break;
+            const double turns = static_cast<double>(j < a.axis_end0 ? p0 : (j < a.axis_end1 ? p1 : p2)) * f[k];
+            sincospif(static_cast<float>(2.0 * (turns - rint(turns))), s_sin + j, s_cos + j);
+        }
+        __syncwarp();
+    }
+};
 
-// weights of q and k, lower and upper half, in lane order: [2][2][D/2]
-template <typename T, int V>
+// weights of q and k: [2][D]
+template <typename T>
 __device__ __forceinline__ void load_weights(const NormRopeArgs &a, float *s_w) {
-    const int half = a.D / 2, lanes = half / V;
-    for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
-        const int qk = i / a.D, d = i - qk * a.D, up = d >= half;
+    for (int i = threadIdx.x; i < 2 * a.D; i += kNormThreads) {
+        const int qk = i >= a.D;
         const T *w = static_cast<const T *>(a.w[qk]);
-        s_w[(qk * 2 + up) * half + lane_slot<V>(d - up * half, lanes)] = w ? to_float(w[d]) : 1.0f;
+        s_w[i] = w ? to_float(w[i - qk * a.D]) : 1.0f;
     }
+    __syncthreads();
 }
 
 template <int GL>
@@ -100,203 +148,275 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-struct NormItem {
-    bool live;
-    int tt, qk, head;
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The heads a warp goes through: tokens u, u + stride, ... (with `share` warps per token each takes every
+// share-th group of kSlots heads), of each token q's heads and then k's. One step is one head per lane group.
+struct NormSteps {
+    int64_t u, units, stride;
+    int share_log2, step;               // step: heads from one to the next
+    int steps_q, steps, at;             // steps of a token, of its q heads; the current one
+    __device__ __forceinline__ void init(const NormRopeArgs &a, int64_t u0, int64_t warps, int slots) {
+        share_log2 = a.share_log2;
+        const int share = 1 << share_log2, part = static_cast<int>(u0) & (share - 1);
+        units = a.L << share_log2;
+        stride = warps;                 // a multiple of share: a warp keeps its part
+        u = u0;
+        step = share * slots;
+        steps_q = (a.heads[0] - part * slots + step - 1) / step;
+        if (steps_q < 0) steps_q = 0;
+        // k's groups are dealt from the share behind the one of q's last group on
+        const int q_groups = (a.heads[0] + slots - 1) / slots;
+        k_first = ((part - q_groups) & (share - 1)) * slots;
+        int steps_k = (a.heads[1] - k_first + step - 1) / step;
+        if (steps_k < 0) steps_k = 0;
+        q_first = part * slots;
+        steps = steps_q + steps_k;
+        at = 0;
+        if (steps == 0) u = units;
+    }
+    int q_first, k_first;
+    __device__ __forceinline__ bool live() const { return u < units; }
+    __device__ __forceinline__ bool is_k() const { return at >= steps_q; }
+    __device__ __forceinline__ int head() const {
+        return at >= steps_q ? k_first + (at - steps_q) * step : q_first + at * step;
+    }
+    __device__ __forceinline__ int64_t token() const { return u >> share_log2; }
+    __device__ __forceinline__ void next() {
+        if (++at == steps) {
+            at = 0;
+            u += stride;
+        }
+    }
 };
-// item i of a tile -> token and head; the q heads of a token first, then its k heads
-__device__ __forceinline__ NormItem norm_item(const NormRopeArgs &a, int i, int tokens, bool lane_live) {
-    const int H = a.heads[0] + a.heads[1];
-    NormItem it;
-    it.tt = i / H;
-    const int h = i - it.tt * H;
-    it.qk = h >= a.heads[0];
-    it.head = it.qk ? h - a.heads[0] : h;
-    it.live = lane_live && it.tt < tokens;
-    return it;
-}
 
-constexpr int kNormHeld = 2;   // items a thread has in flight
-
-template <typename T, int GL>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-    constexpr int V = Vec<T>::kVec;
-    extern __shared__ float4 s_raw[];
-    float *s_cos = reinterpret_cast<float *>(s_raw);
-    float *s_sin = s_cos + a.tile * a.n_freq;
-    float *s_w = s_sin + a.tile * a.n_freq;
-    const int half = a.D / 2, lanes = half / V;
-    const int g = threadIdx.x % GL, slot = threadIdx.x / GL;
-    constexpr int kSlots = kNormThreads / GL;
-    const int64_t l0 = static_cast<int64_t>(blockIdx.x) * a.tile;
-    const int tokens = static_cast<int>(a.L - l0 < a.tile ? a.L - l0 : a.tile);
-    const int n = tokens * (a.heads[0] + a.heads[1]);
-    const bool lane_live = g < lanes;
-
-    auto src = [&](const NormItem &it) {
-        return static_cast<const T *>(a.x[it.qk]) + (l0 + it.tt) * a.xs[it.qk] + it.head * a.D + g * V;
-    };
-    bool ready = false;
-    for (int base = 0; base < n; base += kNormHeld * kSlots) {
-        NormItem it[kNormHeld];
-        uint4 lo[kNormHeld], hi[kNormHeld];
-#pragma unroll
-        for (int u = 0; u < kNormHeld; ++u) {
-            it[u] = norm_item(a, base + u * kSlots + slot, tokens, lane_live);
-            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-            if (it[u].live) {
-                const T *p = src(it[u]);
-                lo[u] = *reinterpret_cast<const uint4 *>(p);
-                hi[u] = *reinterpret_cast<const uint4 *>(p + half);
-            }
-        }
-        if (!ready) {   // the first vectors are in flight while the angles are formed
-            load_weights<T, V>(a, s_w);
-            tile_angles<V>(a, l0, tokens, s_cos, s_sin);
-            __syncthreads();
-            ready = true;
-        }
-#pragma unroll
-        for (int u = 0; u < kNormHeld; ++u) {
-            float xl[V], xh[V];
-            Vec<T>::unpack(lo[u], xl);
-            Vec<T>::unpack(hi[u], xh);
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) ss += xl[e] * xl[e] + xh[e] * xh[e];
-            ss = group_sum<GL>(ss);
-            const float r = rsqrtf(ss / a.D + a.eps);
-            if (it[u].live) {
-                float c[V], s[V], wl[V], wh[V];
-                lane_read<V>(s_cos + it[u].tt * a.n_freq, g, lanes, c);
-                lane_read<V>(s_sin + it[u].tt * a.n_freq, g, lanes, s);
-                lane_read<V>(s_w + it[u].qk * a.D, g, lanes, wl);
-                lane_read<V>(s_w + it[u].qk * a.D + half, g, lanes, wh);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float nl = xl[e] * r * wl[e], nh = xh[e] * r * wh[e];
-                    xl[e] = nl * c[e] - nh * s[e];
-                    xh[e] = nh * c[e] + nl * s[e];
-                }
-                T *p = static_cast<T *>(a.y[it[u].qk]) + (l0 + it[u].tt) * a.ys[it[u].qk] + it[u].head * a.D + g * V;
-                *reinterpret_cast<uint4 *>(p) = Vec<T>::pack(xl);
-                *reinterpret_cast<uint4 *>(p + half) = Vec<T>::pack(xh);
+// One step's vectors into ring slot `slot_at` of this thread (N tensors, two vectors each).
+template <typename T, int N>
+__device__ __forceinline__ void norm_fetch(const NormRopeArgs &a, const NormSteps &st, uint4 *ring, int lane_head,
+                                           int lane_dim, bool lane_live, int half) {
+    if (st.live()) {
+        const int qk = st.is_k(), h = st.head() + lane_head;
+        const int64_t l = st.token();
+        if (lane_live && h < a.heads[qk]) {
+            const T *p = static_cast<const T *>(a.x[qk]) + l * a.xs[qk] + h * a.D + lane_dim;
+            cp_async16(ring, p);
+            cp_async16(ring + kNormThreads, p + half);
+            if (N == 2) {
+                const T *d = static_cast<const T *>(a.dy[qk]) + l * a.dys[qk] + h * a.D + lane_dim;
+                cp_async16(ring + 2 * kNormThreads, d);
+                cp_async16(ring + 3 * kNormThreads, d + half);
             }
         }
     }
+    cp_async_commit();
 }
 
-// Gradient. Persistent CTAs, each a fixed set of tiles (tile blockIdx.x, + gridDim.x, ...), so that
-// the weight gradients are few partial rows, summed in one fixed order whatever the scheduling.
-template <typename T, int GL>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_rope_grad_kernel(const __grid_constant__ NormRopeArgs a) {
-    constexpr int V = Vec<T>::kVec;
-    extern __shared__ float4 s_raw[];
-    float *s_cos = reinterpret_cast<float *>(s_raw);
-    float *s_sin = s_cos + a.tile * a.n_freq;
-    float *s_w = s_sin + a.tile * a.n_freq;
-    const int half = a.D / 2, lanes = half / V;
-    const int g = threadIdx.x % GL, slot = threadIdx.x / GL;
-    constexpr int kSlots = kNormThreads / GL;
-    const bool lane_live = g < lanes;
-    float acc[2][2][V];                 // [q, k][lower, upper]
-#pragma unroll
-    for (int qk = 0; qk < 2; ++qk)
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[qk][0][e] = acc[qk][1][e] = 0.f;
-    load_weights<T, V>(a, s_w);
+constexpr int kNormRing = 7, kNormGradRing = 4;     // steps of a thread's ring
+constexpr int kNormSmem = kNormRing * 2 * kNormThreads * 16, kNormGradSmem = kNormGradRing * 4 * kNormThreads * 16;
 
-    const int64_t n_tiles = (a.L + a.tile - 1) / a.tile;
-    for (int64_t tl = blockIdx.x; tl < n_tiles; tl += gridDim.x) {
-        const int64_t l0 = tl * a.tile;
-        const int tokens = static_cast<int>(a.L - l0 < a.tile ? a.L - l0 : a.tile);
-        const int n = tokens * (a.heads[0] + a.heads[1]);
-        bool ready = false;
-        for (int base = 0; base < n; base += kSlots) {
-            const NormItem it = norm_item(a, base + slot, tokens, lane_live);
-            uint4 v[4];
+template <typename T, int GL>
+__global__ void __launch_bounds__(kNormThreads, 6) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+    constexpr int V = Vec<T>::kVec, P = V / 2, kSlots = 32 / GL;
+    extern __shared__ uint4 s_ring[];               // [step][lower, upper][thread]
+    __shared__ __align__(16) float s_cs[kNormWarps][2][kNormMaxFreq];
+    __shared__ __align__(16) float s_w[4 * kNormMaxFreq];
+    const int half = a.D / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane % GL, slot = lane / GL;
+    const bool lane_live = g * V < half;
+    float *s_cos = s_cs[warp][0], *s_sin = s_cs[warp][1];
+    uint4 *ring = s_ring + threadIdx.x;
+    if (!lane_live)                                  // idle lanes add zeros to their group's sums
+        for (int i = 0; i < 2 * kNormRing; ++i) ring[i * kNormThreads] = make_uint4(0, 0, 0, 0);
+    NormSteps now, ahead;
+    now.init(a, static_cast<int64_t>(blockIdx.x) * kNormWarps + warp, static_cast<int64_t>(gridDim.x) * kNormWarps, kSlots);
+    ahead = now;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = make_uint4(0, 0, 0, 0);
-            if (it.live) {
-                const T *p = static_cast<const T *>(a.x[it.qk]) + (l0 + it.tt) * a.xs[it.qk] + it.head * a.D + g * V;
-                const T *d = static_cast<const T *>(a.dy[it.qk]) + (l0 + it.tt) * a.dys[it.qk] + it.head * a.D + g * V;
-                v[0] = *reinterpret_cast<const uint4 *>(p);
-                v[1] = *reinterpret_cast<const uint4 *>(p + half);
-                v[2] = *reinterpret_cast<const uint4 *>(d);
-                v[3] = *reinterpret_cast<const uint4 *>(d + half);
-            }
-            if (!ready) {
-                __syncthreads();        // the previous tile's angles have been read
-                tile_angles<V>(a, l0, tokens, s_cos, s_sin);
-                __syncthreads();
-                ready = true;
-            }
-            float xl[V], xh[V], dl[V], dh[V], wl[V], wh[V];
-            Vec<T>::unpack(v[0], xl);
-            Vec<T>::unpack(v[1], xh);
-            Vec<T>::unpack(v[2], dl);
-            Vec<T>::unpack(v[3], dh);
-            float ss = 0.f, gx = 0.f;
-            if (it.live) {
-                float c[V], s[V];
-                lane_read<V>(s_cos + it.tt * a.n_freq, g, lanes, c);
-                lane_read<V>(s_sin + it.tt * a.n_freq, g, lanes, s);
-                lane_read<V>(s_w + it.qk * a.D, g, lanes, wl);
-                lane_read<V>(s_w + it.qk * a.D + half, g, lanes, wh);
+    for (int i = 0; i < kNormRing - 1; ++i) {
+        norm_fetch<T, 1>(a, ahead, ring + i * 2 * kNormThreads, slot, g * V, lane_live, half);
+        ahead.next();
+    }
+    LaneFreqs fr;
+    fr.load(a, lane);
+    load_weights<T>(a, s_w);
+    f2 A[P], B[P], C[P], E[P];
+    int at = 0;
+    for (; now.live(); now.next()) {
+        const int qk = now.is_k();
+        const int64_t l = now.token();
+        const bool first = now.at == 0;
+        if (first) fr.angles(a, l, lane, s_cos, s_sin);
+        if ((first || now.at == now.steps_q) && lane_live) {
+            // turn and weights in one: y_lo = r (A x_lo + B x_hi), y_hi = r (C x_hi + E x_lo)
+            f2 c[P], s[P], wl[P], wh[P];
+            lane_read<V>(s_cos, g, c);
+            lane_read<V>(s_sin, g, s);
+            lane_read<V>(s_w + qk * a.D, g, wl);
+            lane_read<V>(s_w + qk * a.D + half, g, wh);
+            const f2 minus = f2_of(-1.f, -1.f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float nl = dl[e] * c[e] + dh[e] * s[e], nh = dh[e] * c[e] - dl[e] * s[e];
-                    dl[e] = nl;
-                    dh[e] = nh;
-                    ss += xl[e] * xl[e] + xh[e] * xh[e];
-                    gx += nl * wl[e] * xl[e] + nh * wh[e] * xh[e];
-                }
-            }
-            ss = group_sum<GL>(ss);
-            gx = group_sum<GL>(gx);
-            if (it.live) {
-                const float r = rsqrtf(ss / a.D + a.eps);
-                const float k = gx / a.D * r * r;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float tl_ = dl[e] * xl[e] * r, th_ = dh[e] * xh[e] * r;
-                    if (it.qk) {
-                        acc[1][0][e] += tl_;
-                        acc[1][1][e] += th_;
-                    } else {
-                        acc[0][0][e] += tl_;
-                        acc[0][1][e] += th_;
-                    }
-                    xl[e] = r * (dl[e] * wl[e] - xl[e] * k);
-                    xh[e] = r * (dh[e] * wh[e] - xh[e] * k);
-                }
-                T *p = static_cast<T *>(a.y[it.qk]) + (l0 + it.tt) * a.ys[it.qk] + it.head * a.D + g * V;
-                *reinterpret_cast<uint4 *>(p) = Vec<T>::pack(xl);
-                *reinterpret_cast<uint4 *>(p + half) = Vec<T>::pack(xh);
+            for (int e = 0; e < P; ++e) {
+                A[e] = f2_mul(wl[e], c[e]);
+                B[e] = f2_mul(f2_mul(wh[e], s[e]), minus);
+                C[e] = f2_mul(wh[e], c[e]);
+                E[e] = f2_mul(wl[e], s[e]);
             }
         }
+        cp_async_wait<kNormRing - 2>();
+        f2 xl[P], xh[P], ss = f2_of(0.f, 0.f);
+        unpack_f2<T>(ring[at * 2 * kNormThreads], xl);
+        unpack_f2<T>(ring[(at * 2 + 1) * kNormThreads], xh);
+        // the slot read one step ago is free: fetch into it
+        norm_fetch<T, 1>(a, ahead, ring + (at == 0 ? kNormRing - 1 : at - 1) * 2 * kNormThreads, slot, g * V, lane_live, half);
+        ahead.next();
+        at = at == kNormRing - 1 ? 0 : at + 1;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            ss = f2_fma(xl[e], xl[e], ss);
+            ss = f2_fma(xh[e], xh[e], ss);
+        }
+        const float r = rsqrtf(group_sum<GL>(f2_sum(ss)) * a.inv_d + a.eps);
+        const f2 r2 = f2_of(r, r);
+        const int h = now.head() + slot;
+        if (lane_live && h < a.heads[qk]) {
+            f2 yl[P], yh[P];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                yl[e] = f2_mul(f2_fma(xh[e], B[e], f2_mul(xl[e], A[e])), r2);
+                yh[e] = f2_mul(f2_fma(xl[e], E[e], f2_mul(xh[e], C[e])), r2);
+            }
+            T *dst = static_cast<T *>(a.y[qk]) + l * a.ys[qk] + h * a.D + g * V;
+            *reinterpret_cast<uint4 *>(dst) = pack_f2<T>(yl);
+            *reinterpret_cast<uint4 *>(dst + half) = pack_f2<T>(yh);
+        }
     }
+    cp_async_wait<0>();
+}
+
+// Gradient. Each warp takes a fixed set of tokens, so that the weight gradients are few partial rows,
+// summed in one fixed order whatever the scheduling.
+template <typename T, int GL>
+__global__ void __launch_bounds__(kNormThreads, 4) norm_rope_grad_kernel(const __grid_constant__ NormRopeArgs a) {
+    constexpr int V = Vec<T>::kVec, P = V / 2, kSlots = 32 / GL;
+    extern __shared__ uint4 s_ring[];               // [step][x lower, upper, dy lower, upper][thread]
+    __shared__ __align__(16) float s_cs[kNormWarps][2][kNormMaxFreq];
+    __shared__ __align__(16) float s_w[4 * kNormMaxFreq];
+    const int half = a.D / 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane % GL, slot = lane / GL;
+    const bool lane_live = g * V < half;
+    float *s_cos = s_cs[warp][0], *s_sin = s_cs[warp][1];
+    uint4 *ring = s_ring + threadIdx.x;
+    NormSteps now, ahead;
+    now.init(a, static_cast<int64_t>(blockIdx.x) * kNormWarps + warp, static_cast<int64_t>(gridDim.x) * kNormWarps, kSlots);
+    ahead = now;
+#pragma unroll
+    for (int i = 0; i < kNormGradRing - 1; ++i) {
+        norm_fetch<T, 2>(a, ahead, ring + i * 4 * kNormThreads, slot, g * V, lane_live, half);
+        ahead.next();
+    }
+    LaneFreqs fr;
+    fr.load(a, lane);
+    load_weights<T>(a, s_w);
+    f2 acc[2][2][P];                     // [q, k][lower, upper half]
+#pragma unroll
+    for (int e = 0; e < P; ++e) acc[0][0][e] = acc[0][1][e] = acc[1][0][e] = acc[1][1][e] = f2_of(0.f, 0.f);
+    const f2 minus = f2_of(-1.f, -1.f);
+    f2 c[P], s[P], wl[P], wh[P];
+    int at = 0;
+    for (; now.live(); now.next()) {
+        const int qk = now.is_k();
+        const int64_t l = now.token();
+        const bool first = now.at == 0;
+        if (first) fr.angles(a, l, lane, s_cos, s_sin);
+        if ((first || now.at == now.steps_q) && lane_live) {
+            lane_read<V>(s_cos, g, c);
+            lane_read<V>(s_sin, g, s);
+            lane_read<V>(s_w + qk * a.D, g, wl);
+            lane_read<V>(s_w + qk * a.D + half, g, wh);
+        }
+        cp_async_wait<kNormGradRing - 2>();
+        f2 xl[P], xh[P], dl[P], dh[P], ss = f2_of(0.f, 0.f), gx = ss;
+        unpack_f2<T>(ring[at * 4 * kNormThreads], xl);
+        unpack_f2<T>(ring[(at * 4 + 1) * kNormThreads], xh);
+        unpack_f2<T>(ring[(at * 4 + 2) * kNormThreads], dl);
+        unpack_f2<T>(ring[(at * 4 + 3) * kNormThreads], dh);
+        norm_fetch<T, 2>(a, ahead, ring + (at == 0 ? kNormGradRing - 1 : at - 1) * 4 * kNormThreads, slot, g * V,
+                         lane_live, half);
+        ahead.next();
+        at = at == kNormGradRing - 1 ? 0 : at + 1;
+        const int h = now.head() + slot;
+        const bool live = lane_live && h < a.heads[qk];
+        if (live) {
+#pragma unroll
+            for (int e = 0; e < P; ++e) {   // dn = R^T dy, then both sums of the head
+                const f2 nl = f2_fma(dh[e], s[e], f2_mul(dl[e], c[e]));
+                dh[e] = f2_fma(f2_mul(dl[e], s[e]), minus, f2_mul(dh[e], c[e]));
+                dl[e] = nl;
+                ss = f2_fma(xl[e], xl[e], ss);
+                ss = f2_fma(xh[e], xh[e], ss);
+                gx = f2_fma(f2_mul(dl[e], wl[e]), xl[e], gx);
+                gx = f2_fma(f2_mul(dh[e], wh[e]), xh[e], gx);
+            }
+        }
+        const float sst = group_sum<GL>(f2_sum(ss)), gxt = group_sum<GL>(f2_sum(gx));
+        if (live) {
+            const float r = rsqrtf(sst * a.inv_d + a.eps), k = -(gxt * a.inv_d * r * r);
+            const f2 r2 = f2_of(r, r), k2 = f2_of(k, k);
+            if (qk == 0) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    acc[0][0][e] = f2_fma(f2_mul(dl[e], r2), xl[e], acc[0][0][e]);
+                    acc[0][1][e] = f2_fma(f2_mul(dh[e], r2), xh[e], acc[0][1][e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    acc[1][0][e] = f2_fma(f2_mul(dl[e], r2), xl[e], acc[1][0][e]);
+                    acc[1][1][e] = f2_fma(f2_mul(dh[e], r2), xh[e], acc[1][1][e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                xl[e] = f2_mul(f2_fma(xl[e], k2, f2_mul(dl[e], wl[e])), r2);
+                xh[e] = f2_mul(f2_fma(xh[e], k2, f2_mul(dh[e], wh[e])), r2);
+            }
+            T *dst = static_cast<T *>(a.y[qk]) + l * a.ys[qk] + h * a.D + g * V;
+            *reinterpret_cast<uint4 *>(dst) = pack_f2<T>(xl);
+            *reinterpret_cast<uint4 *>(dst + half) = pack_f2<T>(xh);
+        }
+    }
+    cp_async_wait<0>();
     if (a.dw_part == nullptr) return;
     // the CTA's partial: groups of a warp by shuffles, warps through shared memory, in warp order
-    __syncthreads();
-    float *s_red = reinterpret_cast<float *>(s_raw);               // [warps][2][D]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();                                 // the rings are read out
+    float(*s_red)[4 * kNormMaxFreq] = reinterpret_cast<float(*)[4 * kNormMaxFreq]>(s_ring);   // [warps]
+    static_assert(kNormWarps * 4 * kNormMaxFreq * 4 <= kNormGradSmem, "the sums fit in the rings");
 #pragma unroll
     for (int qk = 0; qk < 2; ++qk)
 #pragma unroll
         for (int up = 0; up < 2; ++up)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float v = acc[qk][up][e];
+            for (int e = 0; e < P; ++e) {
+                float v[2];
+                f2_get(acc[qk][up][e], v[0], v[1]);
 #pragma unroll
-                for (int o = 16; o >= GL; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane < GL && lane_live) s_red[(warp * 2 + qk) * a.D + up * half + g * V + e] = v;
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int o = 16; o >= GL; o >>= 1) v[b] += __shfl_xor_sync(0xffffffffu, v[b], o);
+                    if (lane < GL && lane_live) s_red[warp][qk * a.D + up * half + g * V + 2 * e + b] = v[b];
+                }
             }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * a.D; i += kNormThreads) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kNormThreads / 32; ++w) v += s_red[w * 2 * a.D + i];
+        for (int w = 0; w < kNormWarps; ++w) v += s_red[w][i];
         a.dw_part[static_cast<int64_t>(blockIdx.x) * 2 * a.D + i] = v;
     }
 }
@@ -309,8 +429,10 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__
     const int c = threadIdx.x & 31, rg = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
     float v = 0.f;
-    if (col < 2 * D)
+    if (col < 2 * D) {
+#pragma unroll 8
         for (int p = rg; p < n_part; p += 32) v += part[static_cast<int64_t>(p) * 2 * D + col];
+    }
     s[rg][c] = v;
     __syncthreads();
     if (rg == 0 && col < 2 * D) {
@@ -339,46 +461,57 @@ int group_lanes(int D, int dtype) {
     return gl;
 }
 
-// Tokens per tile: enough (token, head) items for every lane group of a CTA to hold `held`, at most
-// kNormMaxTile (rows of few heads would otherwise leave most of a CTA idle).
-int tile_tokens(int gl, int heads, int held) {
-    const int want = vitk::kNormThreads / gl * held;
-    return std::max(1, std::min(vitk::kNormMaxTile, want / std::max(1, heads)));
+// Warps per token, 1, 2 or 4: few tokens, or a last round that few warps would have, share heads out
+// (3211 tokens of 32 heads on 2368 warps: two rounds of whole tokens, or three of halves).
+int token_share(int64_t L, int heads, int gl, int ctas) {
+    const int most = std::max(1, (heads * gl + 31) / 32);
+    const int64_t warps = int64_t(ctas) * vitk::kNormWarps;
+    double best = 1e30;
+    int pick = 1;
+    for (int share = 1; share <= vitk::kNormWarps && share <= most; share *= 2) {   // powers of two: a warp keeps its part
+        // rounds of the resident warps, each a token's share and its angles (about a twentieth of a token)
+        const double cost = static_cast<double>((L * share + warps - 1) / warps) * (1.0 / share + 0.05);
+        if (cost < best) {
+            best = cost;
+            pick = share;
+        }
+    }
+    return pick;
 }
 
 template <typename T>
-cudaError_t forward(const vitk::NormRopeArgs &a, int gl, unsigned grid, size_t smem, cudaStream_t s) {
+cudaError_t forward(const vitk::NormRopeArgs &a, int gl, unsigned grid, cudaStream_t s) {
     switch (gl) {
         case 1:   // 16 dims of a 16-bit type; 32-bit heads have two lanes or more
-            if constexpr (sizeof(T) == 2) vitk::norm_rope_kernel<T, 1><<<grid, vitk::kNormThreads, smem, s>>>(a);
+            if constexpr (sizeof(T) == 2) vitk::norm_rope_kernel<T, 1><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a);
             break;
-        case 2: vitk::norm_rope_kernel<T, 2><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
-        case 4: vitk::norm_rope_kernel<T, 4><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
-        case 8: vitk::norm_rope_kernel<T, 8><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
-        case 16: vitk::norm_rope_kernel<T, 16><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
+        case 2: vitk::norm_rope_kernel<T, 2><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
+        case 4: vitk::norm_rope_kernel<T, 4><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
+        case 8: vitk::norm_rope_kernel<T, 8><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
+        case 16: vitk::norm_rope_kernel<T, 16><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
         default:  // 32 lanes: fp32 heads of more than 128 dims
-            if constexpr (sizeof(T) == 4) vitk::norm_rope_kernel<T, 32><<<grid, vitk::kNormThreads, smem, s>>>(a);
+            if constexpr (sizeof(T) == 4) vitk::norm_rope_kernel<T, 32><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a);
     }
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t backward(const vitk::NormRopeArgs &a, int gl, unsigned grid, size_t smem, cudaStream_t s) {
+cudaError_t backward(const vitk::NormRopeArgs &a, int gl, unsigned grid, cudaStream_t s) {
     switch (gl) {
         case 1:   // 16 dims of a 16-bit type; 32-bit heads have two lanes or more
-            if constexpr (sizeof(T) == 2) vitk::norm_rope_grad_kernel<T, 1><<<grid, vitk::kNormThreads, smem, s>>>(a);
+            if constexpr (sizeof(T) == 2) vitk::norm_rope_grad_kernel<T, 1><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a);
             break;
-        case 2: vitk::norm_rope_grad_kernel<T, 2><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
-        case 4: vitk::norm_rope_grad_kernel<T, 4><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
-        case 8: vitk::norm_rope_grad_kernel<T, 8><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
-        case 16: vitk::norm_rope_grad_kernel<T, 16><<<grid, vitk::kNormThreads, smem, s>>>(a); break;
+        case 2: vitk::norm_rope_grad_kernel<T, 2><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
+        case 4: vitk::norm_rope_grad_kernel<T, 4><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
+        case 8: vitk::norm_rope_grad_kernel<T, 8><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
+        case 16: vitk::norm_rope_grad_kernel<T, 16><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
         default:  // 32 lanes: fp32 heads of more than 128 dims
-            if constexpr (sizeof(T) == 4) vitk::norm_rope_grad_kernel<T, 32><<<grid, vitk::kNormThreads, smem, s>>>(a);
+            if constexpr (sizeof(T) == 4) vitk::norm_rope_grad_kernel<T, 32><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a);
     }
     return cudaGetLastError();
 }
 
-void fill(vitk::NormRopeArgs &a, const NormRopeCall &c, int tile) {
+void fill(vitk::NormRopeArgs &a, const NormRopeCall &c, int share) {
     for (int i = 0; i < 2; ++i) {
         a.x[i] = c.x[i];
         a.y[i] = c.y[i];
@@ -393,19 +526,19 @@ void fill(vitk::NormRopeArgs &a, const NormRopeCall &c, int tile) {
     a.eps = c.eps;
     a.pos = c.pos;
     a.L = c.L;
-    a.tile = tile;
+    a.share_log2 = share == 4 ? 2 : share == 2 ? 1 : 0;
+    a.inv_d = 1.0f / c.head_dim;
     a.dw_part = nullptr;
     a.n_freq = c.head_dim / 2;
     a.axis_end0 = c.sections[0];
     a.axis_end1 = c.sections[0] + c.sections[1];
-    // powers of theta^(-2/D), one product each: j roundings of 2^-53, under 2e-14 relative at j = 128
-    // (10^-9 rad at position 10^5), where one pow per frequency would cost a call 2 us on the host
-    const double step = std::pow(c.theta, -2.0 / c.head_dim);
-    double f = 1.0;
-    for (int j = 0; j < a.n_freq; ++j, f *= step) a.inv_freq[j] = f;
+    double f = std::pow(c.theta, -2.0 / c.head_dim);
+    for (int b = 0; b < 7; ++b, f *= f) a.power[b] = f;
 }
 
-size_t angle_bytes(int tile, int D) { return sizeof(float) * (static_cast<size_t>(tile) * D + 2 * D); }
+unsigned cta_count(const vitk::NormRopeArgs &a, int most) {
+    return static_cast<unsigned>(std::min<int64_t>(((a.L << a.share_log2) + vitk::kNormWarps - 1) / vitk::kNormWarps, most));
+}
 
 }  // namespace
 
@@ -414,12 +547,11 @@ int norm_rope_launch(const NormRopeCall &c, cudaStream_t s) {
     if (c.L <= 0 || H <= 0) return VIT_OK;
     const int gl = group_lanes(c.head_dim, c.dtype);
     vitk::NormRopeArgs a;
-    fill(a, c, tile_tokens(gl, H, vitk::kNormHeld));
-    const unsigned grid = static_cast<unsigned>((c.L + a.tile - 1) / a.tile);
-    const size_t smem = angle_bytes(a.tile, c.head_dim);
-    const cudaError_t e = c.dtype == VIT_DTYPE_BF16   ? forward<__nv_bfloat16>(a, gl, grid, smem, s)
-                          : c.dtype == VIT_DTYPE_F16 ? forward<__half>(a, gl, grid, smem, s)
-                                                     : forward<float>(a, gl, grid, smem, s);
+    fill(a, c, token_share(c.L, H, gl, vitk::kNormCtas));
+    const unsigned grid = cta_count(a, vitk::kNormCtas);
+    const cudaError_t e = c.dtype == VIT_DTYPE_BF16   ? forward<__nv_bfloat16>(a, gl, grid, s)
+                          : c.dtype == VIT_DTYPE_F16 ? forward<__half>(a, gl, grid, s)
+                                                     : forward<float>(a, gl, grid, s);
     return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
@@ -433,15 +565,12 @@ int norm_rope_grad_launch(const NormRopeCall &c, float *dqw, float *dkw, void *w
     if (c.L > 0 && H > 0) {
         const int gl = group_lanes(c.head_dim, c.dtype);
         vitk::NormRopeArgs a;
-        fill(a, c, tile_tokens(gl, H, 1));
+        fill(a, c, token_share(c.L, H, gl, vitk::kNormGradCtas));
         a.dw_part = dqw || dkw ? static_cast<float *>(workspace) : nullptr;
-        const int64_t tiles = (c.L + a.tile - 1) / a.tile;
-        grid = static_cast<unsigned>(std::min<int64_t>(tiles, vitk::kNormGradCtas));
-        const size_t smem = std::max(angle_bytes(a.tile, c.head_dim),
-                                     sizeof(float) * (vitk::kNormThreads / 32) * 2 * c.head_dim);
-        const cudaError_t e = c.dtype == VIT_DTYPE_BF16   ? backward<__nv_bfloat16>(a, gl, grid, smem, s)
-                              : c.dtype == VIT_DTYPE_F16 ? backward<__half>(a, gl, grid, smem, s)
-                                                         : backward<float>(a, gl, grid, smem, s);
+        grid = cta_count(a, vitk::kNormGradCtas);
+        const cudaError_t e = c.dtype == VIT_DTYPE_BF16   ? backward<__nv_bfloat16>(a, gl, grid, s)
+                              : c.dtype == VIT_DTYPE_F16 ? backward<__half>(a, gl, grid, s)
+                                                         : backward<float>(a, gl, grid, s);
         if (e != cudaSuccess) return VIT_ERR_CUDA;
     }
     if (dqw || dkw) {   // no tokens: the sums over nothing are written as zeros
