@@ -495,31 +495,28 @@ def _place(dev: int, stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: _stream(None))
 
 
-def _heads_arg(x, what: str):
-    """[L, heads, head_dim] with heads contiguous -> (pointer, token stride, heads)."""
-    if x is None:
-        return None, 0, 0
-    L, H, D = x.shape
-    st = x.stride()
-    if not ((st[1] == D or H == 1) and (st[2] == 1 or D == 1)):
-        raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return x.data_ptr(), (st[0] if L > 1 else H * D), H
+def _rows_arg(t, L: int, H: int, D: int, what: str) -> int:
+    """Token stride of t [L, H, D], whose heads must be contiguous."""
+    s0, s1, s2 = t.stride()
+    if (s1 == D or H == 1) and (s2 == 1 or D == 1):
+        return s0 if L > 1 else H * D
+    raise ValueError(f"{what}: the heads of a token must be contiguous")
+
+
+def _out_rows(x, out, L: int, H: int, D: int, what: str):
+    """``out``, or a new contiguous tensor like x [L, H, D], and its token stride."""
+    if out is None:
+        return x.new_empty((L, H, D)), H * D
+    _need(out.shape == x.shape and out.dtype == x.dtype and out.get_device() == x.get_device(),
+          f"{what} must have its input's shape, type and device")
+    return out, _rows_arg(out, L, H, D, what)
 
 
 def _key_strides(t):
     """Strides of [..., tokens, heads, head_dim] in elements; those of dimensions of one element, which
     torch leaves arbitrary, become head_dim."""
-    return tuple(t.shape[-1] if n == 1 else s for n, s in zip(t.shape, t.stride()))
-
-
-def _like(x, out, what: str):
-    """``out``, or a new contiguous tensor like x (None for None)."""
-    if out is None:
-        return None if x is None else x.new_empty(x.shape)
-    _need(x is not None, f"{what} given without its input")
-    _need(out.shape == x.shape and out.dtype == x.dtype and out.get_device() == x.get_device(),
-          f"{what} must have its input's shape, type and device")
-    return out
+    st = t.stride()
+    return tuple(t.shape[-1] if n == 1 else s for n, s in zip(t.shape, st)) if 1 in t.shape else st
 
 
 def _status_arg(status):
@@ -534,21 +531,29 @@ def _sections_arg(sections):
     return (ctypes.c_int32 * 3)(*sections)
 
 
+_NORM_OPERANDS = ("q and k must be [L, heads, head_dim] of the same tokens, head_dim and type (bf16, fp16 or fp32), pos "
+                  "contiguous int32 [3, L], weights contiguous [head_dim] of the type of q and k")
+
+
 def _norm_args(q, k, pos, q_weight, k_weight):
+    """(L, H, Hk, D, dtype code) of the operands of the norm calls; H or Hk is 0 for a missing q or k."""
     x = k if q is None else q
-    _need(x is not None and x.dim() == 3, "q or k must be given, [L, heads, head_dim]")
-    L, _, D = x.shape
-    dt = DTYPES.get(x.dtype)
-    _need(dt is not None, "q and k must be bf16, fp16 or fp32")
-    if k is not None and k is not x:
-        _need(k.dim() == 3 and k.shape[0] == L and k.shape[2] == D and k.dtype == x.dtype,
-              "q and k must have the same tokens, head_dim and type")
-    _need(pos.dtype == torch.int32 and pos.shape == (3, L) and pos.is_contiguous(), "pos must be contiguous int32 [3, L]")
-    for w in (q_weight, k_weight):
-        if w is not None:
-            _need(w.dtype == x.dtype and w.shape == (D,) and w.is_contiguous(),
-                  "weights must be [head_dim] of the type of q and k")
-    return x, L, D, dt
+    _need(x is not None, "q or k must be given")
+    _need(x.dim() == 3, _NORM_OPERANDS)
+    L, H, D = x.shape
+    t = x.dtype
+    Hk = 0
+    if q is None:
+        H, Hk = 0, H
+    elif k is not None:
+        _need(k.dim() == 3 and k.dtype == t, _NORM_OPERANDS)
+        Lk, Hk, Dk = k.shape
+        _need(Lk == L and Dk == D, _NORM_OPERANDS)
+    if not (t in DTYPES and pos.dtype == torch.int32 and pos.shape == (3, L) and pos.is_contiguous()
+            and (q_weight is None or (q_weight.dtype == t and q_weight.shape == (D,) and q_weight.is_contiguous()))
+            and (k_weight is None or (k_weight.dtype == t and k_weight.shape == (D,) and k_weight.is_contiguous()))):
+        raise ValueError(_NORM_OPERANDS)
+    return L, H, Hk, D, DTYPES[t]
 
 
 def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6, theta: float = MROPE_THETA,
@@ -557,17 +562,23 @@ def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6,
     pass (either may be None; token strides are free, so slices of a packed QKV product work); weights
     [head_dim] or None (ones); pos int32 [3, L]. Returns (q_out, k_out): new tensors, or the given
     ones, which may be q and k themselves."""
-    x, L, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
+    L, H, Hk, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
+    _need((q is not None or q_out is None) and (k is not None or k_out is None), "an output is given without its input")
     dev = _device_of(q, k, pos, q_weight, k_weight)
+    qp = kp = qo = ko = None
+    qs = ks = qos = kos = 0
     with _place(dev, stream):
-        q_out, k_out = _like(q, q_out, "q_out"), _like(k, k_out, "k_out")
-        qp, qs, H = _heads_arg(q, "q")
-        kp, ks, Hk = _heads_arg(k, "k")
-        qo, qos, _ = _heads_arg(q_out, "q_out")
-        ko, kos, _ = _heads_arg(k_out, "k_out")
-        check(lib().mrope_norm_apply(qp, qs, qo, qos, H, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight), _ptr(k_weight),
-                                     eps, pos.data_ptr(), L, theta, _sections_arg(tuple(sections)), _raw_stream(dev)),
-              "mrope_norm_apply")
+        if q is not None:
+            qp, qs = q.data_ptr(), _rows_arg(q, L, H, D, "q")
+            q_out, qos = _out_rows(q, q_out, L, H, D, "q_out")
+            qo = q_out.data_ptr()
+        if k is not None:
+            kp, ks = k.data_ptr(), _rows_arg(k, L, Hk, D, "k")
+            k_out, kos = _out_rows(k, k_out, L, Hk, D, "k_out")
+            ko = k_out.data_ptr()
+        rc = lib().mrope_norm_apply(qp, qs, qo, qos, H, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight), _ptr(k_weight), eps,
+                                    pos.data_ptr(), L, theta, _sections_arg(tuple(sections)), _raw_stream(dev))
+    check(rc, "mrope_norm_apply")
     return q_out, k_out
 
 
@@ -576,30 +587,40 @@ def mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight=None, k_weight=None, eps
                     stream=None):
     """Gradient of ``mrope_norm_apply`` at the same q, k, weights and positions: (dq, dk, dq_weight,
     dk_weight), the weights' in fp32 (None with weight_grads False, or for a missing q or k)."""
-    x, L, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
-    for g, t in ((dq_out, q), (dk_out, k)):
-        _need((g is None) == (t is None) and (g is None or (g.shape == t.shape and g.dtype == t.dtype)),
-              "the outputs' gradients must have the shape and type of q and k")
+    L, H, Hk, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
+    _need((dq_out is None) == (q is None) and (dk_out is None) == (k is None) and (q is not None or dq is None)
+          and (k is not None or dk is None), "gradients go with q and k")
     dev = _device_of(q, k, pos, q_weight, k_weight, dq_out, dk_out)
+    qp = kp = qo = ko = gq = gk = dwq = dwk = wq = wk = ws = None
+    qs = ks = qos = kos = gqs = gks = ws_bytes = 0
+    L_ = lib()
     with _place(dev, stream):
-        dq, dk = _like(q, dq, "dq"), _like(k, dk, "dk")
-        dwq = dwk = ws = None
-        ws_bytes = 0
+        if q is not None:
+            _need(dq_out.shape == q.shape and dq_out.dtype == q.dtype, "dq_out must have q's shape and type")
+            qp, qs = q.data_ptr(), _rows_arg(q, L, H, D, "q")
+            gq, gqs = dq_out.data_ptr(), _rows_arg(dq_out, L, H, D, "dq_out")
+            dq, qos = _out_rows(q, dq, L, H, D, "dq")
+            qo = dq.data_ptr()
+        if k is not None:
+            _need(dk_out.shape == k.shape and dk_out.dtype == k.dtype, "dk_out must have k's shape and type")
+            kp, ks = k.data_ptr(), _rows_arg(k, L, Hk, D, "k")
+            gk, gks = dk_out.data_ptr(), _rows_arg(dk_out, L, Hk, D, "dk_out")
+            dk, kos = _out_rows(k, dk, L, Hk, D, "dk")
+            ko = dk.data_ptr()
         if weight_grads:
-            ws_bytes = lib().mrope_norm_grad_workspace(D)
-            ws = x.new_empty((ws_bytes,), dtype=torch.uint8)
-            dwq = None if q is None else x.new_empty((D,), dtype=torch.float32)
-            dwk = None if k is None else x.new_empty((D,), dtype=torch.float32)
-        gq, gqs, _ = _heads_arg(dq_out, "dq_out")
-        gk, gks, _ = _heads_arg(dk_out, "dk_out")
-        qp, qs, H = _heads_arg(q, "q")
-        kp, ks, Hk = _heads_arg(k, "k")
-        qo, qos, _ = _heads_arg(dq, "dq")
-        ko, kos, _ = _heads_arg(dk, "dk")
-        check(lib().mrope_norm_grad(gq, gqs, qp, qs, qo, qos, H, gk, gks, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight),
-                                    _ptr(k_weight), _ptr(dwq), _ptr(dwk), eps, pos.data_ptr(), L, theta,
-                                    _sections_arg(tuple(sections)), _ptr(ws), ws_bytes, _raw_stream(dev)),
-              "mrope_norm_grad")
+            ws_bytes = L_.mrope_norm_grad_workspace(D)
+            space = pos.new_empty(ws_bytes // 4)
+            ws = space.data_ptr()
+            if q is not None:
+                dwq = q.new_empty(D, dtype=torch.float32)
+                wq = dwq.data_ptr()
+            if k is not None:
+                dwk = k.new_empty(D, dtype=torch.float32)
+                wk = dwk.data_ptr()
+        rc = L_.mrope_norm_grad(gq, gqs, qp, qs, qo, qos, H, gk, gks, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight),
+                                _ptr(k_weight), wq, wk, eps, pos.data_ptr(), L, theta, _sections_arg(tuple(sections)), ws,
+                                ws_bytes, _raw_stream(dev))
+    check(rc, "mrope_norm_grad")
     return dq, dk, dwq, dwk
 
 
@@ -682,39 +703,39 @@ def prefix_attention(q, prefix_k=None, prefix_v=None, k=None, v=None, lens=None,
     with contiguous head_dim (head-major caches as permuted views). cu_q and lens are read on the device.
     max_q defaults to 1 without cu_q, else to total_q; max_len to the capacity. With ``causal`` query j
     of n sees its sequence's keys s <= lens - n + j. Returns (out, lse): out like q, lse fp32 [total_q, heads]."""
-    _need(q.dim() == 3 and q.dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16 [total_q, heads, head_dim]")
+    _need(q.dim() == 3, "q must be bf16 or fp16 [total_q, heads, head_dim]")
     T, H, D = q.shape
     dtype = q.dtype
+    dt = DTYPES.get(dtype, 2)
+    _need(dt != 2, "q must be bf16 or fp16 [total_q, heads, head_dim]")
     _need((prefix_k is None) == (prefix_v is None) and (k is None) == (v is None), "keys and values go together")
-    _need(prefix_k is not None or k is not None, "a prefix or own keys must be given")
     _need((k is None) == (lens is None), "own keys need their lengths")
-    Lp = B = None
-    Hk = (prefix_k if prefix_k is not None else k).shape[-2]
+    Lp, B, Hk = 0, None, None
     pk_token = pk_head = pv_token = pv_head = k_seq = k_token = k_head = v_seq = v_token = v_head = 0
     pk = pv = kp = vp = lp = None
     if prefix_k is not None:
-        Lp = prefix_k.shape[0]
-        i0, i1 = prefix_k.stride(2), prefix_v.stride(2)
-        _need(prefix_k.shape == (Lp, Hk, D) and prefix_v.shape == (Lp, Hk, D) and prefix_k.dtype == dtype
-              and prefix_v.dtype == dtype and ((i0 == 1 and i1 == 1) or D == 1),
+        Lp, Hk, Dk = prefix_k.shape
+        pk_token, pk_head, i0 = _key_strides(prefix_k)
+        pv_token, pv_head, i1 = _key_strides(prefix_v)
+        _need(Dk == D and prefix_v.shape == prefix_k.shape and prefix_k.dtype == dtype and prefix_v.dtype == dtype
+              and ((i0 == 1 and i1 == 1) or D == 1),
               "prefix keys and values must be [prefix_len, kv_heads, head_dim] of q's type, head_dim contiguous")
-        pk_token, pk_head, _ = _key_strides(prefix_k)
-        pv_token, pv_head, _ = _key_strides(prefix_v)
         if Lp:
             pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
     if k is not None:
-        B, cap = k.shape[0], k.shape[1]
-        i0, i1 = k.stride(3), v.stride(3)
-        _need(k.shape == (B, cap, Hk, D) and v.shape == (B, cap, Hk, D) and k.dtype == dtype and v.dtype == dtype
+        B, cap, h, Dk = k.shape
+        k_seq, k_token, k_head, i0 = _key_strides(k)
+        v_seq, v_token, v_head, i1 = _key_strides(v)
+        _need(Dk == D and (Hk is None or Hk == h) and v.shape == k.shape and k.dtype == dtype and v.dtype == dtype
               and ((i0 == 1 and i1 == 1) or D == 1),
               "own keys and values must be [n_seq, capacity, kv_heads, head_dim] of q's type, head_dim contiguous")
+        Hk = h
         _need(lens.dtype == torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [n_seq]")
         max_len = cap if max_len is None else max_len
         _need(0 <= max_len <= cap, "max_len must be within the capacity")
-        k_seq, k_token, k_head, _ = _key_strides(k)
-        v_seq, v_token, v_head, _ = _key_strides(v)
         if cap:
             kp, vp, lp = k.data_ptr(), v.data_ptr(), lens.data_ptr()
+    _need(Hk is not None, "a prefix or own keys must be given")
     if cu_q is not None:
         _need(cu_q.dtype == torch.int32 and cu_q.dim() == 1 and cu_q.shape[0] >= 2 and cu_q.is_contiguous(),
               "cu_q must be int32 [n_seq + 1]")
@@ -738,17 +759,16 @@ def prefix_attention(q, prefix_k=None, prefix_v=None, k=None, v=None, lens=None,
                   "lse must be fp32 [total_q, heads]")
         if T == 0:
             return out, lse
-        qp, qs, _ = _heads_arg(q, "q")
-        op, os_, _ = _heads_arg(out, "out")
-        d = PrefixAttentionDesc(DTYPES[dtype], H, Hk, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, qp, qs,
-                                op, os_, lse.data_ptr(), T, max_q, _ptr(cu_q), n_seq, pk, pv, Lp or 0, pk_token, pk_head,
-                                pv_token, pv_head, kp, vp, k_seq, k_token, k_head, v_seq, v_token, v_head, lp,
-                                max_len if kp is not None else 0)
+        d = PrefixAttentionDesc(dt, H, Hk, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, q.data_ptr(),
+                                _rows_arg(q, T, H, D, "q"), out.data_ptr(), _rows_arg(out, T, H, D, "out"), lse.data_ptr(),
+                                T, max_q, _ptr(cu_q), n_seq, pk, pv, Lp, pk_token, pk_head, pv_token, pv_head, kp, vp,
+                                k_seq, k_token, k_head, v_seq, v_token, v_head, lp, max_len if kp is not None else 0)
         L = lib()
         ref = ctypes.byref(d)
         ws_bytes = L.prefix_attention_workspace(ref)
-        ws = q.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
-        check(L.prefix_attention(ref, _ptr(ws), ws_bytes, _status_arg(status), _raw_stream(dev)), "prefix_attention")
+        ws = q.new_empty(ws_bytes // 2) if ws_bytes else None
+        rc = L.prefix_attention(ref, _ptr(ws), ws_bytes, _status_arg(status), _raw_stream(dev))
+    check(rc, "prefix_attention")
     return out, lse
 
 
