@@ -26,7 +26,13 @@
 
 namespace vitk {
 
-constexpr int kSmThreads = 128, kSmKeys = 64, kSmStages = 3;
+constexpr int kSmThreads = 128, kSmKeys = 64;
+// Ring depth and CTAs per SM: items of 16 rows are short and wait for their lengths and first keys, so
+// three CTAs with two stages each beat two with three (measured below); 64 rows need the registers.
+template <int WR>
+constexpr int kSmStages = WR == 1 ? 2 : 3;
+template <int WR>
+constexpr int kSmCtas = WR == 1 ? 3 : 2;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -67,22 +73,23 @@ template <int DP>
 constexpr int kSmRow = DP * 2 + 16;
 template <int DP>
 constexpr int kSmTileBytes = kSmKeys * kSmRow<DP>;
-template <int DP>
-constexpr int kSmSmem = kSmStages * 2 * kSmTileBytes<DP>;
+template <int DP, int WR>
+constexpr int kSmSmem = kSmStages<WR> * 2 * kSmTileBytes<DP> + (kSmStages<WR> == 2 ? 16 * kSmRow<DP> : 0);
 
 // kind 0: items over the stacked queries and the prefix; 1: a sequence's items over its own keys
 // (stacked plan) or over prefix and own keys (the other plan)
 template <typename T, int DP, int WR, int WK>
-__global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __grid_constant__ PrefixArgs a, int kind) {
+__global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(const __grid_constant__ PrefixArgs a, int kind) {
     static_assert(WR * WK == kSmThreads / 32, "four warps");
     constexpr int M = 16 * WR, KW = kSmKeys / WK, NT = KW / 8, DT = DP / 8, KS = DP / 16;
-    constexpr int kRow = kSmRow<DP>;
+    constexpr int kRow = kSmRow<DP>, kStages = kSmStages<WR>;
     extern __shared__ uint4 sm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(sm_raw);
     const prefix_attention_desc &d = a.d;
     const PrefixPlan &pl = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp / WK, wk = warp % WK;
     const int D = d.head_dim, G = pl.G;
+    pdl_trigger();
 
     // ---- the item: rows [row0, row0 + rows) of a run of queries, key tiles [t0, t1) of its list
     const int h = blockIdx.x % d.n_kv_heads;
@@ -110,7 +117,10 @@ __global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __gri
         q0 = r.q0;
         n_q = r.n_q;
         len = r.len;
-        if (row0 >= n_q * G) return;
+        if (row0 >= n_q * G) {
+            pdl_wait();
+            return;
+        }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
         part = pl.prefix_splits + sp;
         // keys behind the last row's own position are seen by no row of this tile
@@ -135,18 +145,42 @@ __global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __gri
                           : static_cast<const T *>(d.v) + b * d.v_seq + h * d.v_head + k0 * d.v_token;
         const int64_t ks = pre ? d.prefix_k_token : d.k_token, vs = pre ? d.prefix_v_token : d.v_token;
         const uint32_t sk = smem_u32(sm) + stage * 2 * kSmTileBytes<DP>, sv = sk + kSmTileBytes<DP>;
-        // rows behind the last key and dims behind the head are zeros
+        // a thread copies word c of every kRowsAtOnce-th row; rows behind the last key and dims behind the
+        // head are zeros
+        constexpr int kWords = DP / 8;
+        if constexpr (kSmThreads % kWords == 0) {
+            constexpr int kRowsAtOnce = kSmThreads / kWords;
+            const int c = tid % kWords, r0 = tid / kWords;
+            const T *kr = kp + r0 * ks + c * 8, *vr = vp + r0 * vs + c * 8;
+            const uint32_t at = r0 * kRow + c * 16;
+            const int live = c * 8 < D ? n : 0;
+#pragma unroll
+            for (int i = 0; i < kSmKeys / kRowsAtOnce; ++i) {
+                const bool in = r0 + i * kRowsAtOnce < live;
+                cp16(sk + at + i * kRowsAtOnce * kRow, in ? kr : kp, in);
+                cp16(sv + at + i * kRowsAtOnce * kRow, in ? vr : vp, in);
+                kr += kRowsAtOnce * ks;
+                vr += kRowsAtOnce * vs;
+            }
+        } else {
 #pragma unroll 4
-        for (int i = tid; i < kSmKeys * (DP / 8); i += kSmThreads) {
-            const int r = i / (DP / 8), c = i % (DP / 8);
-            const bool in = r < n && c * 8 < D;
-            cp16(sk + r * kRow + c * 16, in ? kp + r * ks + c * 8 : kp, in);
-            cp16(sv + r * kRow + c * 16, in ? vp + r * vs + c * 8 : vp, in);
+            for (int i = tid; i < kSmKeys * kWords; i += kSmThreads) {
+                const int r = i / kWords, c = i % kWords;
+                const bool in = r < n && c * 8 < D;
+                cp16(sk + r * kRow + c * 16, in ? kp + r * ks + c * 8 : kp, in);
+                cp16(sv + r * kRow + c * 16, in ? vp + r * vs + c * 8 : vp, in);
+            }
         }
     };
 
-    // ---- Q: through the last stage's buffer (not loaded before the loop starts) into registers
-    uint8_t *sq = sm + (kSmStages - 1) * 2 * kSmTileBytes<DP>;
+    // ---- the first keys are on their way before Q is fetched: through the last stage's buffer, which is
+    // not loaded before the loop starts (or its own, behind two stages that may both be), into registers
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (t0 + s < t1) load_tile(t0 + s, s);
+        cp_commit();
+    }
+    uint8_t *sq = sm + (kStages == 2 ? 2 : kStages - 1) * 2 * kSmTileBytes<DP>;
     for (int i = tid; i < M * (DP / 8); i += kSmThreads) {
         const int r = i / (DP / 8), c = i % (DP / 8);
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -154,11 +188,6 @@ __global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __gri
             v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(d.q) + token_of(r) * d.q_stride +
                                                  head_of(r) * D + c * 8);
         *reinterpret_cast<uint4 *>(sq + r * kRow + c * 16) = v;
-    }
-#pragma unroll
-    for (int s = 0; s < kSmStages - 1; ++s) {
-        if (t0 + s < t1) load_tile(t0 + s, s);
-        cp_commit();
     }
     __syncthreads();
     uint32_t qf[KS][4];
@@ -180,12 +209,12 @@ __global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __gri
     }
 
     for (int t = t0; t < t1; ++t) {
-        cp_wait<kSmStages - 2>();
+        cp_wait<kStages - 2>();
         __syncthreads();
-        const int nt = t + kSmStages - 1;
-        if (nt < t1) load_tile(nt, (nt - t0) % kSmStages);
+        const int nt = t + kStages - 1;
+        if (nt < t1) load_tile(nt, (nt - t0) % kStages);
         cp_commit();
-        const uint32_t sk = smem_u32(sm) + (t - t0) % kSmStages * 2 * kSmTileBytes<DP> + wk * KW * kRow;
+        const uint32_t sk = smem_u32(sm) + (t - t0) % kStages * 2 * kSmTileBytes<DP> + wk * KW * kRow;
         const uint32_t sv = sk + kSmTileBytes<DP>;
         float s[NT][4];
 #pragma unroll
@@ -257,7 +286,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __gri
     constexpr int kOP = DP + 4;                                // fp32 row pitch
     float *so = reinterpret_cast<float *>(sm);                 // [WK][M][kOP]
     float *sml = so + WK * M * kOP;                            // [WK][M][2]
-    static_assert((WK * M * kOP + 2 * WK * M) * 4 <= kSmSmem<DP>, "epilogue fits in the ring");
+    static_assert((WK * M * kOP + 2 * WK * M) * 4 <= kSmSmem<DP, WR>, "epilogue fits in the ring");
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -309,6 +338,7 @@ __global__ void __launch_bounds__(kSmThreads, 2) prefix_small_kernel(const __gri
             if (c == 0) pl.part_lse[row] = lse2;
         }
     }
+    pdl_wait();   // done only when the prefix's items are: the join waits for this kernel alone
 }
 
 // One warp per (sequence, query, head): weights from the parts' lse, o joined in fp32, four dims per lane
@@ -324,6 +354,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     const int b = static_cast<int>(t / d.max_q), j = static_cast<int>(t % d.max_q);
     const SeqRange r = seq_range(d, b);
     if (j >= r.n_q) return;
+    pdl_wait();   // the parts are written
     const int64_t token = r.q0 + j;
     const int64_t row = token * d.n_heads + head, pitch = d.total_q * d.n_heads;
     float mx = -INFINITY;
@@ -361,7 +392,7 @@ namespace {
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 template <typename T, int DP, int WR, int WK>
-cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s) {
+cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s) {
     if (items <= 0) return cudaSuccess;
     static bool configured[64] = {};
     int dev = 0;
@@ -369,25 +400,28 @@ cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, cud
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !configured[dev]) {
         e = cudaFuncSetAttribute(vitk::prefix_small_kernel<T, DP, WR, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 vitk::kSmSmem<DP>);
+                                 vitk::kSmSmem<DP, WR>);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
+    if (early)
+        return launch_pdl(vitk::prefix_small_kernel<T, DP, WR, WK>, dim3(static_cast<unsigned>(items)),
+                          dim3(vitk::kSmThreads), vitk::kSmSmem<DP, WR>, s, 1, a, kind);
     vitk::prefix_small_kernel<T, DP, WR, WK>
-        <<<static_cast<unsigned>(items), vitk::kSmThreads, vitk::kSmSmem<DP>, s>>>(a, kind);
+        <<<static_cast<unsigned>(items), vitk::kSmThreads, vitk::kSmSmem<DP, WR>, s>>>(a, kind);
     return cudaGetLastError();
 }
 
 template <typename T, int DP>
-cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, cudaStream_t s) {
-    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, s) : launch_small<T, DP, 4, 1>(a, kind, items, s);
+cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool early, cudaStream_t s) {
+    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, early, s) : launch_small<T, DP, 4, 1>(a, kind, items, early, s);
 }
 
 template <typename T>
-cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, cudaStream_t s) {
-    if (a.d.head_dim <= 64) return small<T, 64>(a, kind, m, items, s);
-    if (a.d.head_dim <= 80) return small<T, 80>(a, kind, m, items, s);
-    return small<T, 128>(a, kind, m, items, s);
+cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool early, cudaStream_t s) {
+    if (a.d.head_dim <= 64) return small<T, 64>(a, kind, m, items, early, s);
+    if (a.d.head_dim <= 80) return small<T, 80>(a, kind, m, items, early, s);
+    return small<T, 128>(a, kind, m, items, early, s);
 }
 
 // One kind of work item: which kernel takes it and how its keys are cut.
@@ -412,17 +446,20 @@ Items shape(int64_t rows) {
 // Cuts the keys of `base` items of `tiles` tiles each so that the waves of CTAs (one per SM of the
 // tensor-core kernel, two of the small one) fill up, against what the parts cost: with more than one, every part writes
 // and the join reads an fp32 row of o, and the join is one more launch (about 4 us).
-void cut(Items &it, int64_t base, int tiles, int64_t part_row_bytes, bool joined, int max_splits) {
+void cut(Items &it, int64_t base, int tiles, int64_t part_row_bytes, bool joined, bool even, int max_splits) {
     const bool tc = it.m == kTcRows;
     const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;
-    const int64_t wave = tc ? 148 : 296;
+    const int64_t wave = tc ? 148 : it.m == 16 ? 148 * vitk::kSmCtas<1> : 148 * vitk::kSmCtas<4>;
     double best = 1e30;
     int pick = 1;
     for (int s = 1; s <= std::min(tiles, max_splits); ++s) {
         const int per = ceil_div(tiles, s);
         if (s > 1 && ceil_div(tiles, per) != s) continue;      // the same parts as a smaller s
-        const double waves = static_cast<double>((base * s + wave - 1) / wave);
-        double us = waves * (per * tile_us + start_us);
+        // equal items of the prefix come in whole waves; a sequence's items differ in length, so the last
+        // one to start, which may be a long one, runs on behind an even share of the rest
+        const double item = per * tile_us + start_us;
+        double us = even ? item * static_cast<double>((base * s + wave - 1) / wave)
+                         : item * (base * s > wave ? static_cast<double>(base * s) / wave * 0.75 + 0.75 : 1.0);
         if (joined || s > 1) us += s * part_row_bytes * 2 / 4.0e6;
         if (!joined && s > 1) us += 4.0;
         if (us < best * 0.98) {
@@ -458,14 +495,14 @@ Plan make_plan(const prefix_attention_desc &d) {
     if (p.stacked) {
         pn.prefix = shape(rows);
         cut(pn.prefix, int64_t(d.n_kv_heads) * ceil_div(rows, pn.prefix.m), ceil_div(d.prefix_len, pn.prefix.keys),
-            part_row_bytes, two_kinds, 64);
+            part_row_bytes, two_kinds, true, 64);
         p.prefix_splits = pn.prefix.splits;
         p.prefix_tiles_per_split = pn.prefix.tiles_per_split;
     }
     if (!p.stacked || own) {
         pn.seq = shape(max_rows);
         const int tiles = (own ? ceil_div(d.max_len, pn.seq.keys) : 0) + (p.stacked ? 0 : ceil_div(d.prefix_len, pn.seq.keys));
-        cut(pn.seq, int64_t(d.n_seq) * d.n_kv_heads * ceil_div(max_rows, pn.seq.m), tiles, part_row_bytes, two_kinds, 64);
+        cut(pn.seq, int64_t(d.n_seq) * d.n_kv_heads * ceil_div(max_rows, pn.seq.m), tiles, part_row_bytes, two_kinds, false, 64);
         p.seq_splits = pn.seq.splits;
         p.min_tiles = pn.seq.splits > 1 ? 2 : 1;
     }
@@ -477,11 +514,12 @@ Plan make_plan(const prefix_attention_desc &d) {
     return pn;
 }
 
-int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, cudaStream_t s) {
+// early: the launch may start while the stream's previous kernel, this call's prefix items, drains
+int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, bool early, cudaStream_t s) {
     if (it.count <= 0) return VIT_OK;
-    if (it.m == kTcRows) return prefix_tc_launch(a, kind, it.count, s);
-    const cudaError_t e = a.d.dtype == VIT_DTYPE_BF16 ? small<__nv_bfloat16>(a, kind, it.m, it.count, s)
-                                                      : small<__half>(a, kind, it.m, it.count, s);
+    if (it.m == kTcRows) return prefix_tc_launch(a, kind, it.count, early, s);
+    const cudaError_t e = a.d.dtype == VIT_DTYPE_BF16 ? small<__nv_bfloat16>(a, kind, it.m, it.count, early, s)
+                                                      : small<__half>(a, kind, it.m, it.count, early, s);
     return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
@@ -500,16 +538,14 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     a.status = status;
     a.p.part_o = static_cast<float *>(workspace);
     a.p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pn.o_bytes);
-    int rc = run_items(a, 0, pn.prefix, s);
-    if (rc == VIT_OK) rc = run_items(a, 1, pn.seq, s);
+    int rc = run_items(a, 0, pn.prefix, false, s);
+    if (rc == VIT_OK) rc = run_items(a, 1, pn.seq, pn.prefix.count > 0, s);
     if (rc != VIT_OK || pn.p.parts == 1) return rc;
     const unsigned grid = static_cast<unsigned>((int64_t(d.n_seq) * d.max_q * d.n_heads + 7) / 8);
-    if (d.dtype == VIT_DTYPE_BF16) {
-        vitk::prefix_join_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-    } else {
-        vitk::prefix_join_kernel<__half><<<grid, 256, 0, s>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+    const cudaError_t e = d.dtype == VIT_DTYPE_BF16
+                              ? launch_pdl(vitk::prefix_join_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, 1, a)
+                              : launch_pdl(vitk::prefix_join_kernel<__half>, dim3(grid), dim3(256), 0, s, 1, a);
+    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
 }  // namespace vith

@@ -72,5 +72,6 @@ namespace vith {
 // The tensor-core kernel (prefix_tc.cu) over `items` work items of `kind` (as prefix_small_kernel's),
 // kTcRows query rows each, in tiles of kTcKeys keys.
 constexpr int kTcRows = 256, kTcKeys = 80;
-int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s);
+// early: the launch may start while the stream's previous kernel drains.
+int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s);
 }  // namespace vith

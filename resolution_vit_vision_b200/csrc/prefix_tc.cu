@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // (descriptors, barrier addresses) in uniform registers, where the products read their operands
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int D = d.head_dim, G = pl.G;
+    pdl_trigger();
 
     // ---- the item (as prefix_small_kernel's)
     const int h = blockIdx.x % d.n_kv_heads;
@@ -109,7 +110,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         q0 = r.q0;
         n_q = r.n_q;
         len = r.len;
-        if (row0 >= n_q * G) return;
+        if (row0 >= n_q * G) {
+            pdl_wait();
+            return;
+        }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
         part = pl.prefix_splits + sp;
         own_keys = len;
@@ -415,6 +419,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     }
 
+    pdl_wait();   // done only when the launch before is: the join waits for this kernel alone
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) __nanosleep(200000);
@@ -442,7 +447,7 @@ int key_map(CUtensorMap *m, const prefix_attention_desc &d, const void *p, int64
 }
 
 template <typename T, int HV>
-cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s) {
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -453,6 +458,9 @@ cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kin
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
+    if (early)
+        return launch_pdl(vitk::prefix_tc_kernel<T, HV>, dim3(static_cast<unsigned>(items)), dim3(vitk::kTcThreads),
+                          vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind);
     vitk::prefix_tc_kernel<T, HV><<<static_cast<unsigned>(items), vitk::kTcThreads, vitk::kTcSmem<HV>, s>>>(
         m[0], m[1], m[2], m[3], a, kind);
     return cudaGetLastError();
@@ -460,7 +468,7 @@ cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kin
 
 }  // namespace
 
-int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStream_t s) {
+int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s) {
     if (items <= 0) return VIT_OK;
     const prefix_attention_desc &d = a.d;
     CUtensorMap m[4];
@@ -484,9 +492,9 @@ int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, cudaStr
     }
     cudaError_t e;
     if (d.dtype == VIT_DTYPE_BF16)
-        e = d.head_dim <= 64 ? launch<__nv_bfloat16, 1>(m, a, kind, items, s) : launch<__nv_bfloat16, 2>(m, a, kind, items, s);
+        e = d.head_dim <= 64 ? launch<__nv_bfloat16, 1>(m, a, kind, items, early, s) : launch<__nv_bfloat16, 2>(m, a, kind, items, early, s);
     else
-        e = d.head_dim <= 64 ? launch<__half, 1>(m, a, kind, items, s) : launch<__half, 2>(m, a, kind, items, s);
+        e = d.head_dim <= 64 ? launch<__half, 1>(m, a, kind, items, early, s) : launch<__half, 2>(m, a, kind, items, early, s);
     return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
