@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
             if (c == 0) pl.part_lse[row] = lse2;
         }
     }
-    pdl_wait();   // done only when the prefix's items are: the join waits for this kernel alone
+    pdl_wait();   // done only when the launch before is: the join waits for the last one alone
 }
 
 // One warp per (sequence, query, head): weights from the parts' lse, o joined in fp32, four dims per lane
@@ -514,7 +514,7 @@ Plan make_plan(const prefix_attention_desc &d) {
     return pn;
 }
 
-// early: the launch may start while the stream's previous kernel, this call's prefix items, drains
+// early: the launch may start while the stream's previous kernel, this call's other items, drains
 int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, bool early, cudaStream_t s) {
     if (it.count <= 0) return VIT_OK;
     if (it.m == kTcRows) return prefix_tc_launch(a, kind, it.count, early, s);
@@ -538,8 +538,10 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     a.status = status;
     a.p.part_o = static_cast<float *>(workspace);
     a.p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pn.o_bytes);
-    int rc = run_items(a, 0, pn.prefix, false, s);
-    if (rc == VIT_OK) rc = run_items(a, 1, pn.seq, pn.prefix.count > 0, s);
+    // the sequences' items first: they differ in length, and the SMs that run out of them start on the
+    // prefix's items, which are all alike
+    int rc = run_items(a, 1, pn.seq, false, s);
+    if (rc == VIT_OK) rc = run_items(a, 0, pn.prefix, pn.seq.count > 0, s);
     if (rc != VIT_OK || pn.p.parts == 1) return rc;
     const unsigned grid = static_cast<unsigned>((int64_t(d.n_seq) * d.max_q * d.n_heads + 7) / 8);
     const cudaError_t e = d.dtype == VIT_DTYPE_BF16

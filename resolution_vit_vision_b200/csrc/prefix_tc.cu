@@ -3,15 +3,18 @@
 // A work item is 256 query rows of one key-value head (a row is a token and one of its G query heads:
 // the queries of the whole batch stacked for the prefix part, or one sequence's) against a range of
 // key tiles, a prefix's and then the sequence's own. The two products of a tile are bound by the
-// softmax between them: per (row, key) one exponential on the MUFU and about five issue slots against
-// 4 head_dim tensor-core FLOPs. So two 128-row tiles A and B share every K / V tile and take turns:
+// softmax between them: one exponential per (row, key) takes the MUFU 1280 cycles per pair of 128-row
+// tiles and 80 keys, the products take the tensor cores about the same, and everything else has to hide
+// behind both. So two 128-row tiles A and B share every K / V tile, and eight warps each do their softmax:
 //   warp 0      TMA producer: K_j and V_j (64-column boxes, 128-byte swizzle; head dims behind head_dim
 //               and keys behind the prefix arrive as zeros) into a 4-deep ring
 //   warps 1, 2  one MMA-issuing warp per query tile: S_x(j) = Q_x K_j^T (M 128, N 80) into tensor memory,
 //               O_x += P_x(j) V_j with P_x from tensor memory; S_x(j + 1) is issued as soon as the
 //               softmax has read S_x(j), so the next scores wait for the softmax and not the reverse
-//   warps 3..10 softmax, one row per thread: online maximum with a lazy rescale (the exponent offset moves
-//               only when the maximum grows by more than 2^8), fp32 sums, P rounded to the element type
+//   warps 3..10 softmax of tile A, 11..18 of B: a warp has 16 rows, four threads per row (the layout of an
+//               accumulator fragment), so a row's maximum is two shuffles and four warps per scheduler
+//               cover each other's latencies. Online maximum with a lazy rescale (the exponent offset
+//               moves only when the maximum grows by more than 2^8), fp32 sums, P rounded to the element type
 // Tensor memory: S and P of both tiles beside two 128-column accumulators leave room for 80 keys per
 // tile (2 x (80 + 40) + 2 x 128 columns of 512). Q is copied by the softmax warps (rows of any token
 // and head, so 256 rows are filled whatever G is).
@@ -26,7 +29,7 @@
 
 namespace vitk {
 
-constexpr int kTcThreads = 352, kTcStages = 4, kTcNK = vith::kTcKeys, kTcM = 128;
+constexpr int kTcThreads = 32 * 19, kTcStages = 4, kTcNK = vith::kTcKeys, kTcM = 128;
 constexpr int kTcQBox = kTcM * 128;                  // 128 rows x 64 columns
 constexpr int kTcKBox = kTcNK * 128;                 // 80 keys x 64 columns
 template <int HV>                                    // 64-column halves of a head: head_dim <= 64 HV
@@ -58,7 +61,7 @@ template <typename T, int HV>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tpk, const __grid_constant__ CUtensorMap tpv,
                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                     const __grid_constant__ PrefixArgs a, int kind) {
+                     const __grid_constant__ PrefixArgs a, int kind, int early) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr int kQTile = HV * kTcQBox, kTile = HV * kTcKBox;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         n_q = r.n_q;
         len = r.len;
         if (row0 >= n_q * G) {
-            pdl_wait();
+            if (early) pdl_wait();
             return;
         }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
@@ -127,24 +130,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int n_kv = t1 - t0;
     const int n_x = rows > kTcM ? 2 : 1;                  // query tiles with rows
 
-    // ---- Q rows of the softmax warps: in flight while barriers and tensor memory are set up. Lane r owns
-    // row r of its warp's 32 (its address, later its scores); lanes fetch a row's 16-byte words together.
-    constexpr int kWords = HV * 8, kRowsAtOnce = 32 / kWords, kLoads = 32 / kRowsAtOnce;
-    const int x = warp >= 3 ? (warp - 3) >> 2 : warp - 1;        // query tile of a softmax or issuing warp
-    const int quarter = warp & 3;                                // tensor-memory lanes 32 * quarter ..
-    const int R = row0 + x * kTcM + quarter * 32 + lane;         // (softmax warps) row of the item's run
+    // ---- Q rows of the softmax warps: in flight while barriers and tensor memory are set up. Lanes r and
+    // r + 16 know row r of the warp's 16 (its address and position); lanes fetch a row's 16-byte words together.
+    constexpr int kWords = HV * 8, kRowsAtOnce = 32 / kWords, kLoads = 16 / kRowsAtOnce;
+    const int x = warp >= 3 ? (warp - 3) >> 3 : warp - 1;        // query tile of a softmax or issuing warp
+    const int first_row = (warp & 3) * 32 + ((warp - 3) & 4) * 4;   // (softmax warps) its rows of the tile: 16 from here
+    const int R = row0 + x * kTcM + first_row + (lane & 15);     // row of the item's run that this lane knows
     const int j = R / G, head = h * G + (R - j * G);
     const int64_t token = q0 + j;
     const bool live_row = warp >= 3 && R < row0 + rows;
-    uint4 qw[kLoads];
+    // the swizzled layout of the products: 16-byte word c of row i goes to c ^ (i & 7); words behind the head
+    // and rows behind the item's last are zeros
+    uint8_t *const q_rows = sQ + x * kQTile + first_row * 128;   // this warp's rows of the tile's first box
     if (warp >= 3) {
         const uint64_t at = live_row ? reinterpret_cast<uint64_t>(static_cast<const T *>(d.q) + token * d.q_stride + head * D) : 0;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            const uint64_t p = __shfl_sync(0xffffffffu, at, u * kRowsAtOnce + lane / kWords);
-            qw[u] = make_uint4(0, 0, 0, 0);
-            if (p != 0 && lane % kWords * 8 < D) qw[u] = reinterpret_cast<const uint4 *>(p)[lane % kWords];
+            const int i = u * kRowsAtOnce + lane / kWords, c = lane % kWords;
+            const uint64_t p = __shfl_sync(0xffffffffu, at, i);
+            const bool in = p != 0 && c * 8 < D;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             smem_u32(q_rows + (c >> 3) * kTcQBox + i * 128 + (((c & 7) ^ (i & 7)) << 4))),
+                         "l"(in ? p + c * 16 : reinterpret_cast<uint64_t>(d.q)), "r"(in ? 16 : 0)
+                         : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
     if (warp == 0 && lane < 4) {                          // the descriptors of the first loads
@@ -157,10 +167,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(kv_empty + s, n_x);                 // released by each active tile's issuer
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(q_full + x, kTcM);
+            mbar_init(q_full + x, 256);
             mbar_init(s_full + x, 1);
-            mbar_init(s_free + x, kTcM);
-            mbar_init(p_full + x, kTcM);
+            mbar_init(s_free + x, 256);
+            mbar_init(p_full + x, 256);
             mbar_init(o_done + x, 1);
         }
         *abort_flag = 0;
@@ -252,174 +262,177 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp < 3 + 4 * n_x) {
-        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    } else if (warp < 3 + 8 * n_x) {
+        const uint32_t lane_off = static_cast<uint32_t>(first_row) << 16;
         const uint32_t tS = tmem + tc_s(x) + lane_off, tP = tmem + tc_p(x) + lane_off, tO = tmem + tc_o(x) + lane_off;
-        uint8_t *const q_rows = sQ + x * kQTile + quarter * 32 * 128;   // this warp's rows of the tile's first half
-        // the swizzled layout of the products: 16-byte word c of row i goes to c ^ (i & 7)
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-            const int i = u * kRowsAtOnce + lane / kWords, c = lane % kWords;
-            *reinterpret_cast<uint4 *>(q_rows + (c >> 3) * kTcQBox + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = qw[u];
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         fence_proxy_async_smem();
         mbar_arrive(q_full + x);
-        const int lim = kind == 0 ? 0 : (d.causal ? min(len, len - n_q + j + 1) : len);
-        const int prefix_len = static_cast<int>(d.prefix_len);
+        // this thread's two rows, lane / 4 and lane / 4 + 8 of the warp's: own keys they see, maximum, sums
+        const int lim_known = kind == 0 ? 0 : (d.causal ? min(len, len - n_q + j + 1) : len);
+        int lim[2];
+        lim[0] = __shfl_sync(0xffffffffu, lim_known, lane >> 2);
+        lim[1] = __shfl_sync(0xffffffffu, lim_known, (lane >> 2) + 8);
+        const int prefix_len = static_cast<int>(d.prefix_len), col0 = (lane & 3) * 2;
         const float scale_log2 = d.scale * kLog2e;
-        float m_used = -INFINITY;
-        float l8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // the row's sum in eight shares
+        float m_used[2] = {-INFINITY, -INFINITY};
+        float l[2][2] = {{0.f, 0.f}, {0.f, 0.f}};          // a row's sum: this thread's even and odd columns
         bool ok = true;
-        // the two groups take turns at the exponentials (named barriers 2 and 3), so one group's loads,
-        // maxima and stores run while the other keeps the MUFU busy; B opens A's first turn
-        const int my_turn = 2 + x, their_turn = 3 - x;
-        if (n_x == 2 && x == 1 && n_kv > 0) named_bar_arrive(2, 256);
         for (int i = 0; i < n_kv; ++i) {
-            // a wait that timed out does not leave the loop: both groups keep taking their turns
             if (!mbar_wait(s_full + x, i & 1, wc)) ok = false;
             __syncwarp();
             tc_fence_after();
-            uint32_t sr[kTcNK];
-            tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(sr));
-            tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
-            tmem_ld16(tS + 64, sr + 64);
+            uint32_t sr[kTcNK / 2];                        // [8-column group][row, row + 8][2 columns]
+            tmem_ld_16x256_x8(tS, sr);
+            tmem_ld_16x256_x2(tS + 64, sr + 32);
             tmem_wait_ld();
             reg_fence32(sr);
-            reg_fence32(sr + 32);
-            reg_fence16(sr + 64);
+            reg_fence8(sr + 32);
             tc_fence_before();
             mbar_arrive(s_free + x);
-            const int valid = t0 + i < n_prefix_tiles ? prefix_len - (t0 + i) * kTcNK : lim - (t0 + i - n_prefix_tiles) * kTcNK;
-            if (__any_sync(0xffffffffu, valid < kTcNK)) {
+            const bool pre = t0 + i < n_prefix_tiles;
+            const int k0 = (pre ? t0 + i : t0 + i - n_prefix_tiles) * kTcNK;
+            const int v0 = (pre ? prefix_len : lim[0]) - k0, v1 = (pre ? prefix_len : lim[1]) - k0;
+            if (__any_sync(0xffffffffu, min(v0, v1) < kTcNK)) {
 #pragma unroll
-                for (int k = 0; k < kTcNK; ++k)
-                    if (k >= valid) sr[k] = __float_as_uint(-INFINITY);
+                for (int g = 0; g < kTcNK / 8; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (g * 8 + col0 + (e & 1) >= (e < 2 ? v0 : v1)) sr[4 * g + e] = __float_as_uint(-INFINITY);
             }
-            float m8[8];
+            float neg_m[2], alpha[2];
+            bool need = false;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(sr[e]);
+            for (int r = 0; r < 2; ++r) {
+                float m[2] = {__uint_as_float(sr[2 * r]), __uint_as_float(sr[2 * r + 1])};
 #pragma unroll
-            for (int k = 8; k + 16 <= kTcNK; k += 16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], __uint_as_float(sr[k + e]), __uint_as_float(sr[k + 8 + e]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], __uint_as_float(sr[kTcNK - 8 + e]));
-            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale_log2;
-            const bool need = mx > m_used + kTcRescale;
-            const float alpha = (i > 0 && need) ? exp2_mufu(m_used - mx) : 1.0f;
-            if (need) {
-                m_used = mx;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) l8[e] *= alpha;
+                for (int g = 1; g < kTcNK / 8; ++g)
+                    m[g & 1] = max3(m[g & 1], __uint_as_float(sr[4 * g + 2 * r]), __uint_as_float(sr[4 * g + 2 * r + 1]));
+                float mx = fmaxf(m[0], m[1]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scale_log2;
+                const bool moves = mx > m_used[r] + kTcRescale;
+                alpha[r] = 1.0f;
+                if (moves) {
+                    alpha[r] = exp2_mufu(m_used[r] - mx);      // 0 at the first visible key
+                    m_used[r] = mx;
+                    l[r][0] *= alpha[r];
+                    l[r][1] *= alpha[r];
+                }
+                need = need || moves;
+                neg_m[r] = m_used[r] == -INFINITY ? 0.f : -m_used[r];   // no visible key yet: every p stays 0
             }
-            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;   // no visible key yet: every p stays 0
-            uint32_t pk[kTcNK / 2];
-            if (n_x == 2) named_bar_sync(my_turn, 256);
+            uint32_t pk[kTcNK / 4];                        // [8-column group][row, row + 8]
 #pragma unroll
-            for (int k = 0; k < kTcNK; k += 8) {
+            for (int g = 0; g < kTcNK / 8; g += 2) {       // eight exponentials in flight
                 float p[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = fmaf(__uint_as_float(sr[k + e]), scale_log2, neg_m);
+                for (int e = 0; e < 8; e += 2)
+                    ffma2(p[e], p[e + 1], __uint_as_float(sr[4 * g + e]), __uint_as_float(sr[4 * g + e + 1]), scale_log2,
+                          scale_log2, neg_m[(e >> 1) & 1], neg_m[(e >> 1) & 1]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) p[e] = exp2_mufu(p[e]);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    l8[(e >> 1) + 4 * ((k >> 3) & 1)] += p[e] + p[e + 1];
-                    pk[(k + e) >> 1] = pack2(p[e], p[e + 1], T());
+                    fadd2(l[(e >> 1) & 1][0], l[(e >> 1) & 1][1], p[e], p[e + 1]);
+                    pk[2 * g + (e >> 1)] = pack2(p[e], p[e + 1], T());
                 }
             }
-            if (n_x == 2 && (x == 0 || i + 1 < n_kv)) named_bar_arrive(their_turn, 256);
             // P_x V of the tile before must be complete before O_x is scaled or P_x overwritten
             if (i > 0) {
                 if (!mbar_wait(o_done + x, (i - 1) & 1, wc)) ok = false;
                 __syncwarp();
                 tc_fence_after();
-                if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-                    for (int c = 0; c < D; c += 16) {
+                if (__any_sync(0xffffffffu, need)) {
+                    for (int c = 0; c < D; c += 32) {
                         uint32_t o[16];
-                        tmem_ld16(tO + c, o);
+                        tmem_ld_16x256_x4(tO + c, o);
                         tmem_wait_ld();
                         reg_fence16(o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st16(tO + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
+                        tmem_st_16x256_x4(tO + c, o);
                     }
                 }
             }
-            tmem_st32(tP, pk);
-            tmem_st8(tP + 32, pk + 32);
+            tmem_st_16x128_x8(tP, pk);
+            tmem_st_16x128_x2(tP + 32, pk + 16);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(p_full + x);
         }
-        const float l = ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
         if (n_kv > 0) ok = mbar_wait(o_done + x, (n_kv - 1) & 1, wc) && ok;
+        __syncwarp();
         tc_fence_after();
         bool live = ok && live_row;
         if (kind == 0 && pl.parts == 1 && d.cu_q != nullptr) live = live && token < d.cu_q[d.n_seq];
-        const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-        const float lse2 = (m_used == -INFINITY ? 0.f : m_used) + log2f(l);
         const int64_t prow = (static_cast<int64_t>(part) * d.total_q + token) * d.n_heads + head;
-        // o through shared memory (this warp's Q rows, no longer read), so that a row leaves in whole
-        // 128-byte lines: columns in two rounds of kCols, lane = row on the way in, lanes = words of a row
-        // on the way out
         const bool whole = pl.parts == 1;
+        float inv[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float sum = l[r][0] + l[r][1];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            inv[r] = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+            // the lane that knows the row writes its lse (-inf where no key was visible)
+            const float lse2 = (m_used[r] == -INFINITY ? 0.f : m_used[r]) + log2f(sum);
+            const float mine = __shfl_sync(0xffffffffu, lse2, (lane & 7) * 4);
+            if (live && (lane >> 3) == r) {
+                if (!whole) {
+                    pl.part_lse[prow] = mine;
+                } else if (d.lse) {
+                    d.lse[token * d.n_heads + head] = mine * kLn2;
+                }
+            }
+        }
+        // o through shared memory (this warp's Q rows, no longer read), so that a row leaves in whole
+        // 128-byte lines: accumulator fragments on the way in, lanes = words of a row on the way out
         const int cols = whole ? HV * 64 : HV * 32;                 // columns per round: 16-byte words of T or float
         const uint64_t to = !live ? 0
                             : whole ? reinterpret_cast<uint64_t>(static_cast<T *>(d.out) + token * d.out_stride + head * D)
                                     : reinterpret_cast<uint64_t>(pl.part_o + prow * D);
+        auto at = [&](int row, int byte) {                          // byte of a row's HV * 128 in the swizzled boxes
+            return q_rows + (byte >> 7) * kTcQBox + row * 128 + ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
+        };
         for (int c0 = 0; c0 < D; c0 += cols) {
             for (int c = 0; c < cols && c0 + c < D; c += 32) {
-                uint32_t o[32];
+                uint32_t o[16];
                 if (n_kv > 0) {
-                    tmem_ld32(tO + c0 + c, o);
+                    tmem_ld_16x256_x4(tO + c0 + c, o);
                     tmem_wait_ld();
-                    reg_fence32(o);
+                    reg_fence16(o);
                 }
-                float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = n_kv > 0 ? __uint_as_float(o[e]) * inv : 0.f;
-                auto put = [&](int w, const uint4 &u) {             // 16-byte word w of row `lane`
-                    *reinterpret_cast<uint4 *>(q_rows + (w >> 3) * kTcQBox + lane * 128 + (((w & 7) ^ (lane & 7)) << 4)) = u;
-                };
-                if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) put((c >> 3) + e, Vec<T>::pack(v + 8 * e));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) put((c >> 2) + e, Vec<float>::pack(v + 4 * e));
+                for (int e = 0; e < 16; e += 2) {
+                    const int r = (e >> 1) & 1, row = (lane >> 2) + 8 * r, col = c + (e >> 2) * 8 + col0;
+                    const float v0 = n_kv > 0 ? __uint_as_float(o[e]) * inv[r] : 0.f;
+                    const float v1 = n_kv > 0 ? __uint_as_float(o[e + 1]) * inv[r] : 0.f;
+                    if (whole) {
+                        *reinterpret_cast<uint32_t *>(at(row, col * 2)) = pack2(v0, v1, T());
+                    } else {
+                        *reinterpret_cast<float2 *>(at(row, col * 4)) = make_float2(v0, v1);
+                    }
                 }
             }
             __syncwarp();
             const int words = min(cols, D - c0) / (whole ? 8 : 4), first = c0 / (whole ? 8 : 4), w = lane % kWords;
-            constexpr int kBatch = 8;                               // words read before the first is stored
-#pragma unroll 1
-            for (int u0 = 0; u0 < kLoads; u0 += kBatch) {
-                uint4 r[kBatch];
-                uint64_t p[kBatch];
+            uint4 r[kLoads];
+            uint64_t p[kLoads];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = (u0 + u) * kRowsAtOnce + lane / kWords;
-                    p[u] = __shfl_sync(0xffffffffu, to, i);
-                    r[u] = *reinterpret_cast<const uint4 *>(q_rows + (w >> 3) * kTcQBox + i * 128 + (((w & 7) ^ (i & 7)) << 4));
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    if (p[u] != 0 && w < words) reinterpret_cast<uint4 *>(p[u])[first + w] = r[u];
+            for (int u = 0; u < kLoads; ++u) {
+                const int i = u * kRowsAtOnce + lane / kWords;
+                p[u] = __shfl_sync(0xffffffffu, to, i);
+                r[u] = *reinterpret_cast<const uint4 *>(at(i, w * 16));
             }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u)
+                if (p[u] != 0 && w < words) reinterpret_cast<uint4 *>(p[u])[first + w] = r[u];
             __syncwarp();
-        }
-        if (live) {
-            if (pl.parts > 1) {
-                pl.part_lse[prow] = lse2;
-            } else if (d.lse) {
-                d.lse[token * d.n_heads + head] = lse2 * kLn2;
-            }
         }
     }
 
-    pdl_wait();   // done only when the launch before is: the join waits for this kernel alone
+    if (early) pdl_wait();   // done only when the launch before is: the join waits for this kernel alone
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) __nanosleep(200000);
@@ -460,9 +473,9 @@ cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kin
     }
     if (early)
         return launch_pdl(vitk::prefix_tc_kernel<T, HV>, dim3(static_cast<unsigned>(items)), dim3(vitk::kTcThreads),
-                          vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind);
+                          vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind, early ? 1 : 0);
     vitk::prefix_tc_kernel<T, HV><<<static_cast<unsigned>(items), vitk::kTcThreads, vitk::kTcSmem<HV>, s>>>(
-        m[0], m[1], m[2], m[3], a, kind);
+        m[0], m[1], m[2], m[3], a, kind, early ? 1 : 0);
     return cudaGetLastError();
 }
 

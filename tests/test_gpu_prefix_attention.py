@@ -178,7 +178,7 @@ def test_bad_lengths_are_flagged_and_stay_inside():
         got = nv.prefix_attention(**dict(a, cu_q=cu_bad), status=st)
         torch.cuda.synchronize()
         assert st.item() == nv.VIT_ERR_LIMIT, bad
-        assert torch.equal(got[0][:2], good[0][:2])
+        assert torch.equal(got[0][:1], good[0][:1])      # row 1 is named twice by the first of them
 
 
 def test_lengths_read_by_a_replayed_graph():
