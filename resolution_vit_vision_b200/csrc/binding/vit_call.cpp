@@ -1,0 +1,427 @@
+// vit_call.cpp -- the Python side of the decoder entry points that a decoding step makes for every layer
+// and token (include/vit_decoder.h): checks of the tensors, allocation of the outputs, the call.
+//
+// Their kernels take 3 to 20 us, and marshalling the same call through ctypes took 9 to 20 us of Python (a
+// property read 0.1 us, a torch.empty 2 us, a converted argument 0.15 us), so the host was what bounded
+// them. The other entry points run long enough, or rarely enough, for ctypes. No arithmetic
+// happens here; every computed number comes from the library's kernels.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../../include/vit_decoder.h"
+#include "../../../include/vit.h"
+
+namespace {
+
+PyObject *g_error = nullptr;   // native.VitError(code, what)
+
+using at::Tensor;
+
+// a tensor argument; None gives nullptr
+const Tensor *tensor(PyObject *o, const char *what) {
+    if (o == Py_None) return nullptr;
+    TORCH_CHECK_VALUE(THPVariable_Check(o), what, " must be a tensor");
+    return &THPVariable_Unpack(o);
+}
+
+int dtype_code(const Tensor &t) {
+    switch (t.scalar_type()) {
+        case at::kBFloat16: return VIT_DTYPE_BF16;
+        case at::kHalf: return VIT_DTYPE_F16;
+        case at::kFloat: return VIT_DTYPE_F32;
+        default: return -1;
+    }
+}
+
+// the GPU that holds all the tensors (null is skipped)
+template <typename... Ts>
+c10::DeviceIndex device_of(const Ts *...ts) {
+    c10::DeviceIndex dev = -1;
+    auto one = [&](const Tensor *t) {
+        if (t == nullptr) return;
+        TORCH_CHECK_VALUE(t->is_cuda(), "tensors must be on a GPU");
+        const c10::DeviceIndex i = t->device().index();
+        TORCH_CHECK_VALUE(dev < 0 || dev == i, "tensors are on different devices");
+        dev = i;
+    };
+    (one(ts), ...);
+    return dev;
+}
+
+const void *ptr(const Tensor *t) { return t == nullptr ? nullptr : t->data_ptr(); }
+
+struct Int32Check {
+    const Tensor *t;
+    bool ok(int64_t n) const {
+        return t->scalar_type() == at::kInt && t->dim() == 1 && t->size(0) == n && t->is_contiguous();
+    }
+};
+
+int32_t *status_ptr(const Tensor *t) {
+    if (t == nullptr) return nullptr;
+    TORCH_CHECK_VALUE(t->scalar_type() == at::kInt && t->numel() >= 1, "status must be int32 [1]");
+    return static_cast<int32_t *>(t->data_ptr());
+}
+
+int64_t integer(PyObject *o) {
+    const int64_t v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw python_error();
+    return v;
+}
+double real(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    return v;
+}
+
+// raises native.VitError for a status other than VIT_OK
+void check(int rc, const char *what) {
+    if (rc == VIT_OK) return;
+    PyObject *e = PyObject_CallFunction(g_error, "is", rc, what);
+    if (e != nullptr) {
+        PyErr_SetObject(g_error, e);
+        Py_DECREF(e);
+    }
+    throw python_error();
+}
+
+// [L, heads, head_dim] with the heads of a token contiguous
+struct Rows {
+    Tensor t;
+    void *p = nullptr;
+    int64_t stride = 0;
+};
+
+Rows rows(const Tensor &t, const char *what) {
+    const int64_t L = t.size(0), H = t.size(1), D = t.size(2);
+    const auto st = t.strides();
+    TORCH_CHECK_VALUE((st[1] == D || H == 1) && (st[2] == 1 || D == 1), what, ": the heads of a token must be contiguous");
+    return Rows{t, t.data_ptr(), L > 1 ? st[0] : H * D};
+}
+
+// `out`, or a new contiguous tensor like x
+Rows out_rows(const Tensor &x, const Tensor *out, const char *what) {
+    if (out == nullptr) {
+        Tensor t = at::empty(x.sizes(), x.options());
+        void *p = t.data_ptr();
+        return Rows{std::move(t), p, x.size(1) * x.size(2)};
+    }
+    TORCH_CHECK_VALUE(out->sizes() == x.sizes() && out->scalar_type() == x.scalar_type() && out->device() == x.device(), what,
+                      " must have its input's shape, type and device");
+    return rows(*out, what);
+}
+
+// what both norm calls take
+struct NormOperands {
+    int64_t L, H = 0, Hk = 0, D;
+    int dtype;
+    int32_t sections[3];
+};
+
+NormOperands norm_operands(const Tensor *q, const Tensor *k, const Tensor *pos, const Tensor *qw, const Tensor *kw,
+                           PyObject *sections) {
+    const char *operands =
+        "q and k must be [L, heads, head_dim] of the same tokens, head_dim and type (bf16, fp16 or fp32), pos contiguous "
+        "int32 [3, L], weights contiguous [head_dim] of the type of q and k";
+    NormOperands n;
+    const Tensor *x = q != nullptr ? q : k;
+    TORCH_CHECK_VALUE(x != nullptr, "q or k must be given");
+    TORCH_CHECK_VALUE(x->dim() == 3, operands);
+    n.L = x->size(0);
+    n.D = x->size(2);
+    n.dtype = dtype_code(*x);
+    if (q != nullptr) n.H = q->size(1);
+    if (k != nullptr) {
+        TORCH_CHECK_VALUE(k->dim() == 3 && k->size(0) == n.L && k->size(2) == n.D && k->scalar_type() == x->scalar_type(),
+                          operands);
+        n.Hk = k->size(1);
+    }
+    TORCH_CHECK_VALUE(n.dtype >= 0 && pos != nullptr && pos->scalar_type() == at::kInt && pos->dim() == 2 && pos->size(0) == 3 &&
+                          pos->size(1) == n.L && pos->is_contiguous() && n.H <= INT32_MAX && n.Hk <= INT32_MAX &&
+                          n.D <= INT32_MAX,
+                      operands);
+    for (const Tensor *w : {qw, kw})
+        TORCH_CHECK_VALUE(w == nullptr || (w->scalar_type() == x->scalar_type() && w->dim() == 1 && w->size(0) == n.D &&
+                                           w->is_contiguous()),
+                          operands);
+    PyObject *seq = PySequence_Fast(sections, "sections must be three integers");
+    if (seq == nullptr) throw python_error();
+    bool ok = PySequence_Fast_GET_SIZE(seq) == 3;
+    for (int i = 0; ok && i < 3; ++i) {
+        const long long v = PyLong_AsLongLong(PySequence_Fast_GET_ITEM(seq, i));
+        ok = !(v == -1 && PyErr_Occurred()) && v >= INT32_MIN && v <= INT32_MAX;
+        n.sections[i] = static_cast<int32_t>(v);
+    }
+    Py_DECREF(seq);
+    PyErr_Clear();
+    TORCH_CHECK_VALUE(ok, "sections must be three integers");
+    return n;
+}
+
+// a new reference to the given tensor object, a wrapped new tensor, or None
+PyObject *give(PyObject *given, Tensor &&made) {
+    if (given != Py_None) return Py_NewRef(given);
+    if (!made.defined()) Py_RETURN_NONE;
+    return THPVariable_Wrap(std::move(made));
+}
+
+PyObject *pack(std::initializer_list<PyObject *> items) {
+    PyObject *t = PyTuple_New(static_cast<Py_ssize_t>(items.size()));
+    Py_ssize_t i = 0;
+    for (PyObject *o : items) {
+        if (o == nullptr || t == nullptr) throw python_error();
+        PyTuple_SET_ITEM(t, i++, o);
+    }
+    return t;
+}
+
+void arity(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK(n == want, "expected ", want, " arguments, got ", n); }
+
+// (q, k, pos, q_weight, k_weight, eps, theta, sections, q_out, k_out) -> (q_out, k_out)
+PyObject *norm_apply(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arity(n, 10);
+    const Tensor *q = tensor(a[0], "q"), *k = tensor(a[1], "k"), *pos = tensor(a[2], "pos"), *qw = tensor(a[3], "q_weight"),
+                 *kw = tensor(a[4], "k_weight"), *qo = tensor(a[8], "q_out"), *ko = tensor(a[9], "k_out");
+    const NormOperands s = norm_operands(q, k, pos, qw, kw, a[7]);
+    TORCH_CHECK_VALUE((q != nullptr || qo == nullptr) && (k != nullptr || ko == nullptr), "an output is given without its input");
+    const auto dev = device_of(q, k, pos, qw, kw);
+    c10::cuda::CUDAGuard guard(dev);
+    Rows rq, rk, oq, ok;
+    if (q != nullptr) {
+        rq = rows(*q, "q");
+        oq = out_rows(*q, qo, "q_out");
+    }
+    if (k != nullptr) {
+        rk = rows(*k, "k");
+        ok = out_rows(*k, ko, "k_out");
+    }
+    check(mrope_norm_apply(rq.p, rq.stride, oq.p, oq.stride, static_cast<int>(s.H), rk.p, rk.stride, ok.p, ok.stride,
+                           static_cast<int>(s.Hk), static_cast<int>(s.D), s.dtype, ptr(qw), ptr(kw),
+                           static_cast<float>(real(a[5])), static_cast<const int32_t *>(ptr(pos)), s.L, real(a[6]), s.sections,
+                           c10::cuda::getCurrentCUDAStream(dev).stream()),
+          "mrope_norm_apply");
+    return pack({give(a[8], std::move(oq.t)), give(a[9], std::move(ok.t))});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dq_out, dk_out, q, k, pos, q_weight, k_weight, eps, theta, sections, dq, dk, weight_grads)
+//   -> (dq, dk, dq_weight, dk_weight)
+PyObject *norm_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arity(n, 13);
+    const Tensor *gq = tensor(a[0], "dq_out"), *gk = tensor(a[1], "dk_out"), *q = tensor(a[2], "q"), *k = tensor(a[3], "k"),
+                 *pos = tensor(a[4], "pos"), *qw = tensor(a[5], "q_weight"), *kw = tensor(a[6], "k_weight"),
+                 *dq = tensor(a[10], "dq"), *dk = tensor(a[11], "dk");
+    const NormOperands s = norm_operands(q, k, pos, qw, kw, a[9]);
+    TORCH_CHECK_VALUE((gq == nullptr) == (q == nullptr) && (gk == nullptr) == (k == nullptr) && (q != nullptr || dq == nullptr) &&
+                          (k != nullptr || dk == nullptr),
+                      "gradients go with q and k");
+    const bool weights = PyObject_IsTrue(a[12]) == 1;
+    const auto dev = device_of(q, k, pos, qw, kw, gq, gk);
+    c10::cuda::CUDAGuard guard(dev);
+    Rows rq, rk, xq, xk, oq, ok;
+    if (q != nullptr) {
+        TORCH_CHECK_VALUE(gq->sizes() == q->sizes() && gq->scalar_type() == q->scalar_type(), "dq_out must have q's shape and type");
+        xq = rows(*q, "q");
+        rq = rows(*gq, "dq_out");
+        oq = out_rows(*q, dq, "dq");
+    }
+    if (k != nullptr) {
+        TORCH_CHECK_VALUE(gk->sizes() == k->sizes() && gk->scalar_type() == k->scalar_type(), "dk_out must have k's shape and type");
+        xk = rows(*k, "k");
+        rk = rows(*gk, "dk_out");
+        ok = out_rows(*k, dk, "dk");
+    }
+    Tensor ws, wq, wk;
+    int64_t ws_bytes = 0;
+    if (weights) {
+        const auto f32 = pos->options().dtype(at::kFloat);
+        ws_bytes = mrope_norm_grad_workspace(static_cast<int>(s.D));
+        ws = at::empty({ws_bytes / 4}, f32);
+        if (q != nullptr) wq = at::empty({s.D}, f32);
+        if (k != nullptr) wk = at::empty({s.D}, f32);
+    }
+    auto f32_ptr = [](const Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; };
+    check(mrope_norm_grad(rq.p, rq.stride, xq.p, xq.stride, oq.p, oq.stride, static_cast<int>(s.H), rk.p, rk.stride, xk.p,
+                          xk.stride, ok.p, ok.stride, static_cast<int>(s.Hk), static_cast<int>(s.D), s.dtype, ptr(qw), ptr(kw),
+                          f32_ptr(wq), f32_ptr(wk), static_cast<float>(real(a[7])), static_cast<const int32_t *>(ptr(pos)), s.L,
+                          real(a[8]), s.sections, f32_ptr(ws), ws_bytes, c10::cuda::getCurrentCUDAStream(dev).stream()),
+          "mrope_norm_grad");
+    return pack({give(a[10], std::move(oq.t)), give(a[11], std::move(ok.t)), give(Py_None, std::move(wq)),
+                 give(Py_None, std::move(wk))});
+    END_HANDLE_TH_ERRORS
+}
+
+// (input_ids, embed_table, vision, scale, out, status) -> out
+PyObject *embed(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arity(n, 6);
+    const Tensor *ids = tensor(a[0], "input_ids"), *table = tensor(a[1], "embed_table"), *vis = tensor(a[2], "vision"),
+                 *out = tensor(a[4], "out"), *status = tensor(a[5], "status");
+    TORCH_CHECK_VALUE(ids != nullptr && ids->scalar_type() == at::kInt && ids->dim() == 1 && ids->is_contiguous(),
+                      "input_ids must be contiguous int32 [L]");
+    TORCH_CHECK_VALUE(table != nullptr && table->dim() == 2 && dtype_code(*table) >= 0 && table->is_contiguous() &&
+                          table->size(1) <= INT32_MAX,
+                      "embed_table must be contiguous [vocab, dim] in bf16, fp16 or fp32");
+    const int64_t L = ids->size(0), D = table->size(1), n_vis = vis != nullptr ? vis->size(0) : 0;
+    TORCH_CHECK_VALUE(vis == nullptr || (vis->scalar_type() == table->scalar_type() && vis->dim() == 2 && vis->size(1) == D &&
+                                         vis->is_contiguous()),
+                      "vision must be contiguous [n_vision, dim] of the table's type");
+    TORCH_CHECK_VALUE(out == nullptr || (out->scalar_type() == table->scalar_type() && out->dim() == 2 && out->size(0) == L &&
+                                         out->size(1) == D && out->is_contiguous()),
+                      "out must be contiguous [L, dim] of the table's type");
+    const auto dev = device_of(table, ids, vis, out, status);
+    c10::cuda::CUDAGuard guard(dev);
+    Tensor made;
+    if (out == nullptr) made = at::empty({L, D}, table->options());
+    check(embed_vision_tokens(static_cast<const int32_t *>(ptr(ids)), L, ptr(table), dtype_code(*table), table->size(0),
+                              static_cast<int>(D), static_cast<float>(real(a[3])), n_vis > 0 ? ptr(vis) : nullptr, n_vis,
+                              out != nullptr ? out->data_ptr() : made.data_ptr(), status_ptr(status),
+                              c10::cuda::getCurrentCUDAStream(dev).stream()),
+          "embed_vision_tokens");
+    return give(a[4], std::move(made));
+    END_HANDLE_TH_ERRORS
+}
+
+// strides of a key or value tensor [..., tokens, heads, head_dim], those of dimensions of one element (which
+// torch leaves arbitrary) replaced by head_dim
+void key_strides(const Tensor &t, int64_t *st) {
+    const int64_t d = t.dim();
+    for (int64_t i = 0; i < d; ++i) st[i] = t.size(i) == 1 && i + 1 < d ? t.size(d - 1) : t.stride(i);
+}
+
+// (q, prefix_k, prefix_v, k, v, lens, cu_q, max_q, max_len, scale, causal, out, lse, status) -> (out, lse)
+PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    arity(n, 14);
+    const Tensor *q = tensor(a[0], "q"), *pk = tensor(a[1], "prefix_k"), *pv = tensor(a[2], "prefix_v"), *k = tensor(a[3], "k"),
+                 *v = tensor(a[4], "v"), *lens = tensor(a[5], "lens"), *cu_q = tensor(a[6], "cu_q"), *out = tensor(a[11], "out"),
+                 *lse = tensor(a[12], "lse"), *status = tensor(a[13], "status");
+    TORCH_CHECK_VALUE(q != nullptr && q->dim() == 3 && (dtype_code(*q) == VIT_DTYPE_BF16 || dtype_code(*q) == VIT_DTYPE_F16),
+                      "q must be bf16 or fp16 [total_q, heads, head_dim]");
+    TORCH_CHECK_VALUE((pk == nullptr) == (pv == nullptr) && (k == nullptr) == (v == nullptr), "keys and values go together");
+    TORCH_CHECK_VALUE(pk != nullptr || k != nullptr, "a prefix or own keys must be given");
+    TORCH_CHECK_VALUE((k == nullptr) == (lens == nullptr), "own keys need their lengths");
+    const int64_t T = q->size(0), H = q->size(1), D = q->size(2);
+    TORCH_CHECK_VALUE(H <= INT32_MAX && D <= INT32_MAX, "q is too large");
+    prefix_attention_desc d{};
+    int64_t Hk = -1, B = -1, st[4];
+    if (pk != nullptr) {
+        TORCH_CHECK_VALUE(pk->dim() == 3 && pk->size(2) == D && pk->sizes() == pv->sizes() &&
+                              pk->scalar_type() == q->scalar_type() && pv->scalar_type() == q->scalar_type() &&
+                              ((pk->stride(2) == 1 && pv->stride(2) == 1) || D == 1) && pk->size(1) <= INT32_MAX,
+                          "prefix keys and values must be [prefix_len, kv_heads, head_dim] of q's type, head_dim contiguous");
+        Hk = pk->size(1);
+        d.prefix_len = pk->size(0);
+        key_strides(*pk, st);
+        d.prefix_k_token = st[0];
+        d.prefix_k_head = st[1];
+        key_strides(*pv, st);
+        d.prefix_v_token = st[0];
+        d.prefix_v_head = st[1];
+        if (d.prefix_len > 0) {
+            d.prefix_k = pk->data_ptr();
+            d.prefix_v = pv->data_ptr();
+        }
+    }
+    if (k != nullptr) {
+        TORCH_CHECK_VALUE(k->dim() == 4 && k->size(3) == D && (Hk < 0 || Hk == k->size(2)) && k->sizes() == v->sizes() &&
+                              k->scalar_type() == q->scalar_type() && v->scalar_type() == q->scalar_type() &&
+                              ((k->stride(3) == 1 && v->stride(3) == 1) || D == 1) && k->size(2) <= INT32_MAX,
+                          "own keys and values must be [n_seq, capacity, kv_heads, head_dim] of q's type, head_dim contiguous");
+        B = k->size(0);
+        Hk = k->size(2);
+        const int64_t capacity = k->size(1);
+        TORCH_CHECK_VALUE((Int32Check{lens}.ok(B)), "lens must be int32 [n_seq]");
+        const int64_t max_len = a[8] == Py_None ? capacity : integer(a[8]);
+        TORCH_CHECK_VALUE(max_len >= 0 && max_len <= capacity, "max_len must be within the capacity");
+        if (capacity > 0) {
+            key_strides(*k, st);
+            d.k_seq = st[0];
+            d.k_token = st[1];
+            d.k_head = st[2];
+            key_strides(*v, st);
+            d.v_seq = st[0];
+            d.v_token = st[1];
+            d.v_head = st[2];
+            d.k = k->data_ptr();
+            d.v = v->data_ptr();
+            d.lens = static_cast<const int32_t *>(lens->data_ptr());
+            d.max_len = max_len;
+        }
+    }
+    int64_t max_q, n_seq;
+    if (cu_q != nullptr) {
+        TORCH_CHECK_VALUE(cu_q->dim() == 1 && cu_q->size(0) >= 2 && (Int32Check{cu_q}.ok(cu_q->size(0))),
+                          "cu_q must be int32 [n_seq + 1]");
+        n_seq = cu_q->size(0) - 1;
+        max_q = a[7] == Py_None ? std::max<int64_t>(T, 1) : integer(a[7]);
+        d.cu_q = static_cast<const int32_t *>(cu_q->data_ptr());
+    } else {
+        max_q = a[7] == Py_None ? 1 : integer(a[7]);
+        n_seq = B >= 0 ? B : T / std::max<int64_t>(max_q, 1);
+        TORCH_CHECK_VALUE(T == 0 || (max_q > 0 && T % max_q == 0 && n_seq == T / max_q),
+                          "without cu_q there must be max_q queries for each sequence");
+    }
+    TORCH_CHECK_VALUE(B < 0 || B == n_seq, "k and cu_q disagree on the number of sequences");
+    TORCH_CHECK_VALUE(n_seq <= INT32_MAX, "too many sequences");
+    TORCH_CHECK_VALUE(lse == nullptr || (lse->scalar_type() == at::kFloat && lse->dim() == 2 && lse->size(0) == T &&
+                                         lse->size(1) == H && lse->is_contiguous()),
+                      "lse must be fp32 [total_q, heads]");
+    const auto dev = device_of(q, pk, pv, k, v, lens, cu_q, out, lse, status);
+    c10::cuda::CUDAGuard guard(dev);
+    Rows o = out_rows(*q, out, "out");
+    Tensor made_lse;
+    if (lse == nullptr) made_lse = at::empty({T, H}, q->options().dtype(at::kFloat));
+    if (T > 0) {
+        const Rows rq = rows(*q, "q");
+        d.dtype = dtype_code(*q);
+        d.n_heads = static_cast<int>(H);
+        d.n_kv_heads = static_cast<int>(Hk);
+        d.head_dim = static_cast<int>(D);
+        d.scale = static_cast<float>(a[9] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : real(a[9]));
+        d.causal = PyObject_IsTrue(a[10]) == 1;
+        d.q = rq.p;
+        d.q_stride = rq.stride;
+        d.out = o.p;
+        d.out_stride = o.stride;
+        d.lse = static_cast<float *>(lse != nullptr ? lse->data_ptr() : made_lse.data_ptr());
+        d.total_q = T;
+        d.max_q = max_q;
+        d.n_seq = static_cast<int>(n_seq);
+        const int64_t bytes = prefix_attention_workspace(&d);
+        Tensor ws;
+        if (bytes > 0) ws = at::empty({(bytes + 3) / 4}, q->options().dtype(at::kFloat));
+        check(prefix_attention(&d, bytes > 0 ? ws.data_ptr() : nullptr, bytes, status_ptr(status),
+                               c10::cuda::getCurrentCUDAStream(dev).stream()),
+              "prefix_attention");
+    }
+    return pack({give(a[11], std::move(o.t)), give(a[12], std::move(made_lse))});
+    END_HANDLE_TH_ERRORS
+}
+
+// (error class): called once by native.py
+PyObject *set_error(PyObject *, PyObject *cls) {
+    Py_XSETREF(g_error, Py_NewRef(cls));
+    Py_RETURN_NONE;
+}
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
+PyMethodDef kMethods[] = {{"norm_apply", FAST(norm_apply), METH_FASTCALL, nullptr},
+                          {"norm_grad", FAST(norm_grad), METH_FASTCALL, nullptr},
+                          {"embed", FAST(embed), METH_FASTCALL, nullptr},
+                          {"attention", FAST(attention), METH_FASTCALL, nullptr},
+                          {"set_error", set_error, METH_O, nullptr},
+                          {nullptr, nullptr, 0, nullptr}};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_vit_call", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__vit_call() { return PyModule_Create(&kModule); }

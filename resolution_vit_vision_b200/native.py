@@ -7,9 +7,7 @@ device is not an sm_100 GPU, the calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import functools
 import os
 from typing import Dict, Optional, Sequence
 
@@ -457,11 +455,24 @@ def scatter_vision_tokens(input_ids, embed_table, vision, out=None, status=None,
 
 
 # ------------------------------------------------------------------------------------------------
-# decoder-side steps with their gradients, and attention over a shared prefix (include/vit_decoder.h).
-# Decoding calls them once per layer and token with kernels of a few microseconds, so the marshalling
-# below reads each tensor property once and allocates with new_empty / empty_like.
+# decoder-side steps with their gradients, and attention over a shared prefix (include/vit_decoder.h)
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_HERE_AND_NOW = contextlib.nullcontext()
+_call_module = None
+
+
+def _call():
+    """The extension module that checks and makes the calls of a decoding step (csrc/binding/vit_call.cpp)."""
+    global _call_module
+    if _call_module is None:
+        lib()
+        try:
+            from . import _vit_call
+        except ImportError as e:
+            raise RuntimeError("_vit_call.so is missing or does not fit this torch: build it with "
+                               "`python -m resolution_vit_vision_b200.build`") from e
+        _vit_call.set_error(VitError)
+        _call_module = _vit_call
+    return _call_module
 
 
 def _need(ok: bool, what: str) -> None:
@@ -469,91 +480,12 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _device_of(*tensors) -> int:
-    """The index of the GPU that holds all the tensors (None is skipped)."""
-    dev = None
+def _on(stream, *tensors):
+    """The context of a call on an explicit stream: it and its device current, so that outputs and
+    workspaces made inside belong to it."""
     for t in tensors:
-        if t is not None:
-            i = t.get_device()
-            if i != dev:
-                _need(dev is None, "tensors are on different devices")
-                _need(i >= 0, "tensors must be on a GPU")
-                dev = i
-    return dev
-
-
-def _place(dev: int, stream):
-    """The context a call on GPU ``dev`` runs in: that GPU current and, where a stream is given, that
-    stream current, so that outputs and workspaces made inside belong to it."""
-    if stream is not None:
-        _need(stream.device.index == dev, "the stream belongs to another device than the tensors")
-        return torch.cuda.stream(stream)
-    return _HERE_AND_NOW if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-
-
-# the current stream's handle without making a torch.cuda.Stream of it (3 us), where torch offers that
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: _stream(None))
-
-
-def _rows_arg(t, L: int, H: int, D: int, what: str) -> int:
-    """Token stride of t [L, H, D], whose heads must be contiguous."""
-    s0, s1, s2 = t.stride()
-    if (s1 == D or H == 1) and (s2 == 1 or D == 1):
-        return s0 if L > 1 else H * D
-    raise ValueError(f"{what}: the heads of a token must be contiguous")
-
-
-def _out_rows(x, out, L: int, H: int, D: int, what: str):
-    """``out``, or a new contiguous tensor like x [L, H, D], and its token stride."""
-    if out is None:
-        return x.new_empty((L, H, D)), H * D
-    _need(out.shape == x.shape and out.dtype == x.dtype and out.get_device() == x.get_device(),
-          f"{what} must have its input's shape, type and device")
-    return out, _rows_arg(out, L, H, D, what)
-
-
-def _key_strides(t):
-    """Strides of [..., tokens, heads, head_dim] in elements; those of dimensions of one element, which
-    torch leaves arbitrary, become head_dim."""
-    st = t.stride()
-    return tuple(t.shape[-1] if n == 1 else s for n, s in zip(t.shape, st)) if 1 in t.shape else st
-
-
-def _status_arg(status):
-    if status is None:
-        return None
-    _need(status.dtype == torch.int32 and status.numel() >= 1, "status must be int32 [1]")
-    return status.data_ptr()
-
-
-@functools.lru_cache(maxsize=64)
-def _sections_arg(sections):
-    return (ctypes.c_int32 * 3)(*sections)
-
-
-_NORM_OPERANDS = ("q and k must be [L, heads, head_dim] of the same tokens, head_dim and type (bf16, fp16 or fp32), pos "
-                  "contiguous int32 [3, L], weights contiguous [head_dim] of the type of q and k")
-
-
-def _norm_args(q, k, pos, q_weight, k_weight):
-    """(L, H, Hk, D, dtype code) of the operands of the norm calls; H or Hk is 0 for a missing q or k."""
-    x = k if q is None else q
-    _need(x is not None, "q or k must be given")
-    _need(x.dim() == 3, _NORM_OPERANDS)
-    L, H, D = x.shape
-    t = x.dtype
-    Hk = 0
-    if q is None:
-        H, Hk = 0, H
-    elif k is not None:
-        _need(k.dim() == 3 and k.dtype == t, _NORM_OPERANDS)
-        Lk, Hk, Dk = k.shape
-        _need(Lk == L and Dk == D, _NORM_OPERANDS)
-    if not (t in DTYPES and pos.dtype == torch.int32 and pos.shape == (3, L) and pos.is_contiguous()
-            and (q_weight is None or (q_weight.dtype == t and q_weight.shape == (D,) and q_weight.is_contiguous()))
-            and (k_weight is None or (k_weight.dtype == t and k_weight.shape == (D,) and k_weight.is_contiguous()))):
-        raise ValueError(_NORM_OPERANDS)
-    return L, H, Hk, D, DTYPES[t]
+        _need(t is None or t.device == stream.device, "the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
 def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6, theta: float = MROPE_THETA,
@@ -562,24 +494,10 @@ def mrope_norm_apply(q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6,
     pass (either may be None; token strides are free, so slices of a packed QKV product work); weights
     [head_dim] or None (ones); pos int32 [3, L]. Returns (q_out, k_out): new tensors, or the given
     ones, which may be q and k themselves."""
-    L, H, Hk, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
-    _need((q is not None or q_out is None) and (k is not None or k_out is None), "an output is given without its input")
-    dev = _device_of(q, k, pos, q_weight, k_weight)
-    qp = kp = qo = ko = None
-    qs = ks = qos = kos = 0
-    with _place(dev, stream):
-        if q is not None:
-            qp, qs = q.data_ptr(), _rows_arg(q, L, H, D, "q")
-            q_out, qos = _out_rows(q, q_out, L, H, D, "q_out")
-            qo = q_out.data_ptr()
-        if k is not None:
-            kp, ks = k.data_ptr(), _rows_arg(k, L, Hk, D, "k")
-            k_out, kos = _out_rows(k, k_out, L, Hk, D, "k_out")
-            ko = k_out.data_ptr()
-        rc = lib().mrope_norm_apply(qp, qs, qo, qos, H, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight), _ptr(k_weight), eps,
-                                    pos.data_ptr(), L, theta, _sections_arg(tuple(sections)), _raw_stream(dev))
-    check(rc, "mrope_norm_apply")
-    return q_out, k_out
+    if stream is not None:
+        with _on(stream, q, k):
+            return mrope_norm_apply(q, k, pos, q_weight, k_weight, eps, theta, sections, q_out, k_out)
+    return _call().norm_apply(q, k, pos, q_weight, k_weight, eps, theta, sections, q_out, k_out)
 
 
 def mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -587,73 +505,19 @@ def mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight=None, k_weight=None, eps
                     stream=None):
     """Gradient of ``mrope_norm_apply`` at the same q, k, weights and positions: (dq, dk, dq_weight,
     dk_weight), the weights' in fp32 (None with weight_grads False, or for a missing q or k)."""
-    L, H, Hk, D, dt = _norm_args(q, k, pos, q_weight, k_weight)
-    _need((dq_out is None) == (q is None) and (dk_out is None) == (k is None) and (q is not None or dq is None)
-          and (k is not None or dk is None), "gradients go with q and k")
-    dev = _device_of(q, k, pos, q_weight, k_weight, dq_out, dk_out)
-    qp = kp = qo = ko = gq = gk = dwq = dwk = wq = wk = ws = None
-    qs = ks = qos = kos = gqs = gks = ws_bytes = 0
-    L_ = lib()
-    with _place(dev, stream):
-        if q is not None:
-            _need(dq_out.shape == q.shape and dq_out.dtype == q.dtype, "dq_out must have q's shape and type")
-            qp, qs = q.data_ptr(), _rows_arg(q, L, H, D, "q")
-            gq, gqs = dq_out.data_ptr(), _rows_arg(dq_out, L, H, D, "dq_out")
-            dq, qos = _out_rows(q, dq, L, H, D, "dq")
-            qo = dq.data_ptr()
-        if k is not None:
-            _need(dk_out.shape == k.shape and dk_out.dtype == k.dtype, "dk_out must have k's shape and type")
-            kp, ks = k.data_ptr(), _rows_arg(k, L, Hk, D, "k")
-            gk, gks = dk_out.data_ptr(), _rows_arg(dk_out, L, Hk, D, "dk_out")
-            dk, kos = _out_rows(k, dk, L, Hk, D, "dk")
-            ko = dk.data_ptr()
-        if weight_grads:
-            ws_bytes = L_.mrope_norm_grad_workspace(D)
-            space = pos.new_empty(ws_bytes // 4)
-            ws = space.data_ptr()
-            if q is not None:
-                dwq = q.new_empty(D, dtype=torch.float32)
-                wq = dwq.data_ptr()
-            if k is not None:
-                dwk = k.new_empty(D, dtype=torch.float32)
-                wk = dwk.data_ptr()
-        rc = L_.mrope_norm_grad(gq, gqs, qp, qs, qo, qos, H, gk, gks, kp, ks, ko, kos, Hk, D, dt, _ptr(q_weight),
-                                _ptr(k_weight), wq, wk, eps, pos.data_ptr(), L, theta, _sections_arg(tuple(sections)), ws,
-                                ws_bytes, _raw_stream(dev))
-    check(rc, "mrope_norm_grad")
-    return dq, dk, dwq, dwk
-
-
-def _ids_arg(input_ids) -> int:
-    _need(input_ids.dtype == torch.int32 and input_ids.dim() == 1 and input_ids.is_contiguous(),
-          "input_ids must be contiguous int32 [L]")
-    return input_ids.shape[0]
+    if stream is not None:
+        with _on(stream, q, k):
+            return mrope_norm_grad(dq_out, dk_out, q, k, pos, q_weight, k_weight, eps, theta, sections, dq, dk, weight_grads)
+    return _call().norm_grad(dq_out, dk_out, q, k, pos, q_weight, k_weight, eps, theta, sections, dq, dk, weight_grads)
 
 
 def embed_vision_tokens(input_ids, embed_table, vision=None, scale: float = 1.0, out=None, status=None, stream=None):
     """The decoder's input rows: scale * embedding for text ids, vision tokens (unscaled) at the image /
     video placeholders. bf16, fp16 or fp32, all of one type."""
-    L = _ids_arg(input_ids)
-    V, D = embed_table.shape
-    dtype = embed_table.dtype
-    dt = DTYPES.get(dtype)
-    _need(dt is not None and embed_table.is_contiguous(), "embed_table must be contiguous bf16, fp16 or fp32")
-    n_vis = 0
-    if vision is not None:
-        n_vis = vision.shape[0]
-        _need(vision.dtype == dtype and vision.shape == (n_vis, D) and vision.is_contiguous(),
-              "vision must be contiguous [n_vision, dim] of the table's type")
-    dev = _device_of(embed_table, input_ids, vision, out, status)
-    with _place(dev, stream):
-        if out is None:
-            out = embed_table.new_empty((L, D))
-        else:
-            _need(out.shape == (L, D) and out.dtype == dtype and out.is_contiguous(),
-                  "out must be contiguous [L, dim] of the table's type")
-        check(lib().embed_vision_tokens(input_ids.data_ptr(), L, embed_table.data_ptr(), dt, V, D, scale,
-                                        vision.data_ptr() if n_vis else None, n_vis, out.data_ptr(),
-                                        _status_arg(status), _raw_stream(dev)), "embed_vision_tokens")
-    return out
+    if stream is not None:
+        with _on(stream, embed_table):
+            return embed_vision_tokens(input_ids, embed_table, vision, scale, out, status)
+    return _call().embed(input_ids, embed_table, vision, scale, out, status)
 
 
 def embed_vision_tokens_grad(input_ids, d_out, vocab: int, n_vision: int = 0, scale: float = 1.0, table_dtype=None,
@@ -661,18 +525,25 @@ def embed_vision_tokens_grad(input_ids, d_out, vocab: int, n_vision: int = 0, sc
     """Gradient of ``embed_vision_tokens``: (d_table [vocab, dim], d_vision [n_vision, dim] or None). d_table
     is of table_dtype (d_out's type, or fp32); a given d_table is overwritten, or added to with
     accumulate (then only the rows that input_ids names are touched)."""
-    L = _ids_arg(input_ids)
-    dtype = d_out.dtype
-    dt = DTYPES.get(dtype)
-    _need(dt is not None and d_out.dim() == 2 and d_out.shape[0] == L and d_out.is_contiguous(),
+    if stream is not None:
+        with _on(stream, d_out):
+            return embed_vision_tokens_grad(input_ids, d_out, vocab, n_vision, scale, table_dtype, d_table, accumulate,
+                                            d_vision, status)
+    _need(input_ids.dtype == torch.int32 and input_ids.dim() == 1 and input_ids.is_contiguous(),
+          "input_ids must be contiguous int32 [L]")
+    L, dtype = input_ids.shape[0], d_out.dtype
+    _need(dtype in DTYPES and d_out.dim() == 2 and d_out.shape[0] == L and d_out.is_contiguous(),
           "d_out must be contiguous [L, dim] in bf16, fp16 or fp32")
     D = d_out.shape[1]
     _need(d_table is not None or not accumulate, "accumulate needs a d_table to add to")
     if table_dtype is None:
         table_dtype = dtype if d_table is None else d_table.dtype
     _need(table_dtype in (dtype, torch.float32), "the table's gradient is of d_out's type or fp32")
-    dev = _device_of(d_out, input_ids, d_table, d_vision, status)
-    with _place(dev, stream):
+    for t in (input_ids, d_out, d_table, d_vision, status):
+        _need(t is None or t.is_cuda, "tensors must be on a GPU")
+        _need(t is None or t.device == d_out.device, "tensors are on different devices")
+    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), "status must be int32 [1]")
+    with torch.cuda.device(d_out.device):
         if d_table is None:
             d_table = d_out.new_empty((vocab, D), dtype=table_dtype)
         _need(d_table.shape == (vocab, D) and d_table.dtype == table_dtype and d_table.is_contiguous(),
@@ -682,13 +553,11 @@ def embed_vision_tokens_grad(input_ids, d_out, vocab: int, n_vision: int = 0, sc
         _need(d_vision is None or (d_vision.shape == (n_vision, D) and d_vision.dtype == dtype
                                    and d_vision.is_contiguous()),
               "d_vision must be contiguous [n_vision, dim] of d_out's type")
-        L_ = lib()
-        ws_bytes = L_.embed_vision_tokens_grad_workspace(L, vocab, D)
+        ws_bytes = lib().embed_vision_tokens_grad_workspace(L, vocab, D)
         ws = d_out.new_empty((ws_bytes,), dtype=torch.uint8)
-        check(L_.embed_vision_tokens_grad(input_ids.data_ptr(), L, d_out.data_ptr(), dt, vocab, D, scale,
-                                          d_table.data_ptr(), DTYPES[table_dtype], 1 if accumulate else 0,
-                                          _ptr(d_vision), n_vision, ws.data_ptr(), ws_bytes, _status_arg(status),
-                                          _raw_stream(dev)), "embed_vision_tokens_grad")
+        check(lib().embed_vision_tokens_grad(_ptr(input_ids), L, _ptr(d_out), DTYPES[dtype], vocab, D, scale, _ptr(d_table),
+                                             DTYPES[table_dtype], 1 if accumulate else 0, _ptr(d_vision), n_vision,
+                                             _ptr(ws), ws_bytes, _ptr(status), _stream(None)), "embed_vision_tokens_grad")
     return d_table, d_vision
 
 
@@ -703,73 +572,10 @@ def prefix_attention(q, prefix_k=None, prefix_v=None, k=None, v=None, lens=None,
     with contiguous head_dim (head-major caches as permuted views). cu_q and lens are read on the device.
     max_q defaults to 1 without cu_q, else to total_q; max_len to the capacity. With ``causal`` query j
     of n sees its sequence's keys s <= lens - n + j. Returns (out, lse): out like q, lse fp32 [total_q, heads]."""
-    _need(q.dim() == 3, "q must be bf16 or fp16 [total_q, heads, head_dim]")
-    T, H, D = q.shape
-    dtype = q.dtype
-    dt = DTYPES.get(dtype, 2)
-    _need(dt != 2, "q must be bf16 or fp16 [total_q, heads, head_dim]")
-    _need((prefix_k is None) == (prefix_v is None) and (k is None) == (v is None), "keys and values go together")
-    _need((k is None) == (lens is None), "own keys need their lengths")
-    Lp, B, Hk = 0, None, None
-    pk_token = pk_head = pv_token = pv_head = k_seq = k_token = k_head = v_seq = v_token = v_head = 0
-    pk = pv = kp = vp = lp = None
-    if prefix_k is not None:
-        Lp, Hk, Dk = prefix_k.shape
-        pk_token, pk_head, i0 = _key_strides(prefix_k)
-        pv_token, pv_head, i1 = _key_strides(prefix_v)
-        _need(Dk == D and prefix_v.shape == prefix_k.shape and prefix_k.dtype == dtype and prefix_v.dtype == dtype
-              and ((i0 == 1 and i1 == 1) or D == 1),
-              "prefix keys and values must be [prefix_len, kv_heads, head_dim] of q's type, head_dim contiguous")
-        if Lp:
-            pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
-    if k is not None:
-        B, cap, h, Dk = k.shape
-        k_seq, k_token, k_head, i0 = _key_strides(k)
-        v_seq, v_token, v_head, i1 = _key_strides(v)
-        _need(Dk == D and (Hk is None or Hk == h) and v.shape == k.shape and k.dtype == dtype and v.dtype == dtype
-              and ((i0 == 1 and i1 == 1) or D == 1),
-              "own keys and values must be [n_seq, capacity, kv_heads, head_dim] of q's type, head_dim contiguous")
-        Hk = h
-        _need(lens.dtype == torch.int32 and lens.shape == (B,) and lens.is_contiguous(), "lens must be int32 [n_seq]")
-        max_len = cap if max_len is None else max_len
-        _need(0 <= max_len <= cap, "max_len must be within the capacity")
-        if cap:
-            kp, vp, lp = k.data_ptr(), v.data_ptr(), lens.data_ptr()
-    _need(Hk is not None, "a prefix or own keys must be given")
-    if cu_q is not None:
-        _need(cu_q.dtype == torch.int32 and cu_q.dim() == 1 and cu_q.shape[0] >= 2 and cu_q.is_contiguous(),
-              "cu_q must be int32 [n_seq + 1]")
-        n_seq = cu_q.shape[0] - 1
-        max_q = max(T, 1) if max_q is None else max_q
-    else:
-        max_q = 1 if max_q is None else max_q
-        n_seq = B if B is not None else T // max(max_q, 1)
-        _need(n_seq * max_q == T or T == 0, "without cu_q there must be max_q queries for each sequence")
-    _need(B is None or B == n_seq, "k and cu_q disagree on the number of sequences")
-    dev = _device_of(q, prefix_k, prefix_v, k, v, lens, cu_q, out, lse, status)
-    with _place(dev, stream):
-        if out is None:
-            out = q.new_empty((T, H, D))
-        else:
-            _need(out.shape == q.shape and out.dtype == dtype, "out must have q's shape and type")
-        if lse is None:
-            lse = q.new_empty((T, H), dtype=torch.float32)
-        else:
-            _need(lse.shape == (T, H) and lse.dtype == torch.float32 and lse.is_contiguous(),
-                  "lse must be fp32 [total_q, heads]")
-        if T == 0:
-            return out, lse
-        d = PrefixAttentionDesc(dt, H, Hk, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, q.data_ptr(),
-                                _rows_arg(q, T, H, D, "q"), out.data_ptr(), _rows_arg(out, T, H, D, "out"), lse.data_ptr(),
-                                T, max_q, _ptr(cu_q), n_seq, pk, pv, Lp, pk_token, pk_head, pv_token, pv_head, kp, vp,
-                                k_seq, k_token, k_head, v_seq, v_token, v_head, lp, max_len if kp is not None else 0)
-        L = lib()
-        ref = ctypes.byref(d)
-        ws_bytes = L.prefix_attention_workspace(ref)
-        ws = q.new_empty(ws_bytes // 2) if ws_bytes else None
-        rc = L.prefix_attention(ref, _ptr(ws), ws_bytes, _status_arg(status), _raw_stream(dev))
-    check(rc, "prefix_attention")
-    return out, lse
+    if stream is not None:
+        with _on(stream, q):
+            return prefix_attention(q, prefix_k, prefix_v, k, v, lens, cu_q, max_q, max_len, scale, causal, out, lse, status)
+    return _call().attention(q, prefix_k, prefix_v, k, v, lens, cu_q, max_q, max_len, scale, causal, out, lse, status)
 
 
 def op_wait_selftest(status, limit_cycles: int, stream=None):
