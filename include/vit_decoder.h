@@ -142,8 +142,11 @@ typedef struct {
 
 /* workspace: prefix_attention_workspace(desc) bytes (host-only; 0 for a bad descriptor) of device
  * memory, 16-byte aligned, not shared with work that may run at the same time; it depends on sizes
- * alone, not on what cu_q and lens hold. Data errors (a length outside [0, max_len], query ranges that
- * leave [0, total_q] or are longer than max_q) write VIT_ERR_LIMIT to dev_status (int32 [1] device, or
+ * alone, not on what cu_q and lens hold. The call's kernels are laid out for max_q queries and max_len
+ * own keys of every sequence: bounds far above what cu_q and lens hold cost time. As with the encoder's
+ * kernels, one that the caller launches next with programmatic stream serialisation may start early
+ * and has to wait (griddepcontrol.wait) before it touches what the call reads or writes. Data errors (a length outside [0, max_len], query ranges that
+ * do not start at 0, leave [0, total_q], run backwards or are longer than max_q) write VIT_ERR_LIMIT to dev_status (int32 [1] device, or
  * NULL); the values are clamped, nothing outside the buffers is touched, and the rows concerned
  * are not meaningful. A kernel wait that timed out writes VIT_ERR_TIMEOUT there. */
 int64_t prefix_attention_workspace(const prefix_attention_desc *desc);

@@ -80,6 +80,12 @@ double real(PyObject *o) {
     return v;
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v != 0;
+}
+
 // raises native.VitError for a status other than VIT_OK
 void check(int rc, const char *what) {
     if (rc == VIT_OK) return;
@@ -223,7 +229,7 @@ PyObject *norm_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     TORCH_CHECK_VALUE((gq == nullptr) == (q == nullptr) && (gk == nullptr) == (k == nullptr) && (q != nullptr || dq == nullptr) &&
                           (k != nullptr || dk == nullptr),
                       "gradients go with q and k");
-    const bool weights = PyObject_IsTrue(a[12]) == 1;
+    const bool weights = truth(a[12]);
     const auto dev = device_of(q, k, pos, qw, kw, gq, gk);
     c10::cuda::CUDAGuard guard(dev);
     Rows rq, rk, xq, xk, oq, ok;
@@ -387,7 +393,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         d.n_kv_heads = static_cast<int>(Hk);
         d.head_dim = static_cast<int>(D);
         d.scale = static_cast<float>(a[9] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : real(a[9]));
-        d.causal = PyObject_IsTrue(a[10]) == 1;
+        d.causal = truth(a[10]);
         d.q = rq.p;
         d.q_stride = rq.stride;
         d.out = o.p;

@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
     int row0, t0, t1, n_prefix_tiles, own_keys = 0;
     const int prefix_tiles = static_cast<int>((d.prefix_len + kSmKeys - 1) / kSmKeys);
     if (kind == 0) {
+        check_ranges(a);
         part = rest % pl.prefix_splits;
         row0 = rest / pl.prefix_splits * M;
         q0 = 0;
@@ -341,41 +342,67 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
     pdl_wait();   // done only when the launch before is: the join waits for the last one alone
 }
 
-// One warp per (sequence, query, head): weights from the parts' lse, o joined in fp32, four dims per lane
-template <typename T>
-__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+// Joins the parts of a row (sequence, query, head): weights from the parts' lse, o in fp32, four dims per
+// lane. W warps share a row, each with every W-th part, and meet in shared memory: a row of forty parts read
+// by one warp took 8 us of latency. Parts without keys were not written: they are read all the same (the
+// loads need not wait for the weights) and dropped by their weight of 0.
+constexpr int kJoinWarps = 8;
+
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+    __shared__ float4 s_o[kJoinWarps][32];
+    __shared__ float s_w[kJoinWarps];
     const prefix_attention_desc &d = a.d;
     const PrefixPlan &pl = a.p;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (w >= static_cast<int64_t>(d.n_seq) * d.max_q * d.n_heads) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp) / W;
+    const bool inside = w < static_cast<int64_t>(d.n_seq) * d.max_q * d.n_heads;
     const int head = static_cast<int>(w % d.n_heads);
-    const int64_t t = w / d.n_heads;
+    const int64_t t = inside ? w / d.n_heads : 0;
     const int b = static_cast<int>(t / d.max_q), j = static_cast<int>(t % d.max_q);
     const SeqRange r = seq_range(d, b);
-    if (j >= r.n_q) return;
+    const bool live = inside && j < r.n_q;
     pdl_wait();   // the parts are written
     const int64_t token = r.q0 + j;
     const int64_t row = token * d.n_heads + head, pitch = d.total_q * d.n_heads;
-    float mx = -INFINITY;
-    for (int i = lane; i < pl.parts; i += 32) mx = fmaxf(mx, pl.part_lse[i * pitch + row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float off = mx == -INFINITY ? 0.f : mx;
+    float off = 0.f, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+    if (live) {
+        float mx = -INFINITY;
+        for (int i = lane; i < pl.parts; i += 32) mx = fmaxf(mx, pl.part_lse[i * pitch + row]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        off = mx == -INFINITY ? 0.f : mx;
+        const bool has = lane * 4 < d.head_dim;
+        const float *o = pl.part_o + row * d.head_dim + lane * 4;
 #pragma unroll 4
-    for (int i = 0; i < pl.parts; ++i) {
-        const float wt = exp2f(pl.part_lse[i * pitch + row] - off);
-        sum += wt;
-        if (wt != 0.f && lane * 4 < d.head_dim) {      // a part without keys was not written
-            const float4 v = *reinterpret_cast<const float4 *>(pl.part_o + (i * pitch + row) * d.head_dim + lane * 4);
-            acc.x += wt * v.x;
-            acc.y += wt * v.y;
-            acc.z += wt * v.z;
-            acc.w += wt * v.w;
+        for (int i = sub; i < pl.parts; i += W) {
+            const float wt = exp2f(pl.part_lse[i * pitch + row] - off);
+            const float4 v = has ? *reinterpret_cast<const float4 *>(o + i * pitch * d.head_dim) : acc;
+            const bool use = wt != 0.f;
+            sum += wt;
+            acc.x += use ? wt * v.x : 0.f;
+            acc.y += use ? wt * v.y : 0.f;
+            acc.z += use ? wt * v.z : 0.f;
+            acc.w += use ? wt * v.w : 0.f;
         }
     }
+    if (W > 1) {
+        s_o[warp][lane] = acc;
+        if (lane == 0) s_w[warp] = sum;
+        __syncthreads();
+        if (sub != 0) return;
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const float4 v = s_o[warp + i][lane];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+            sum += s_w[warp + i];
+        }
+    }
+    if (!live) return;
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
     if (lane * 4 < d.head_dim)
         *reinterpret_cast<uint2 *>(static_cast<T *>(d.out) + token * d.out_stride + head * d.head_dim + lane * 4) =
@@ -459,7 +486,7 @@ void cut(Items &it, int64_t base, int tiles, int64_t part_row_bytes, bool joined
         // one to start, which may be a long one, runs on behind an even share of the rest
         const double item = per * tile_us + start_us;
         double us = even ? item * static_cast<double>((base * s + wave - 1) / wave)
-                         : item * (base * s > wave ? static_cast<double>(base * s) / wave * 0.75 + 0.75 : 1.0);
+                         : item * (1.0 + 0.6 * std::max(0.0, static_cast<double>(base * s) / wave - 1.0));
         if (joined || s > 1) us += s * part_row_bytes * 2 / 4.0e6;
         if (!joined && s > 1) us += 4.0;
         if (us < best * 0.98) {
@@ -514,6 +541,24 @@ Plan make_plan(const prefix_attention_desc &d) {
     return pn;
 }
 
+template <typename T, int W>
+cudaError_t launch_join(const vitk::PrefixArgs &a, cudaStream_t s) {
+    const int64_t rows = int64_t(a.d.n_seq) * a.d.max_q * a.d.n_heads;
+    return launch_pdl(vitk::prefix_join_kernel<T, W>, dim3(static_cast<unsigned>(ceil_div(rows * W, vitk::kJoinWarps))),
+                      dim3(32 * vitk::kJoinWarps), 0, s, 1, a);
+}
+
+// Several warps per row where that still is one wave of CTAs (eight per SM): 28 rows of 43 parts 26.7 ->
+// 22.5 us a call, while eight warps for each of 7168 rows of 6 parts made 117 us of it 133.
+template <typename T>
+int join(const vitk::PrefixArgs &a, cudaStream_t s) {
+    const int64_t rows = int64_t(a.d.n_seq) * a.d.max_q * a.d.n_heads, wave = 148 * 8;
+    const cudaError_t e = a.p.parts > 4 && rows <= wave       ? launch_join<T, 8>(a, s)
+                          : a.p.parts > 4 && rows <= 2 * wave ? launch_join<T, 4>(a, s)
+                                                              : launch_join<T, 1>(a, s);
+    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+}
+
 // early: the launch may start while the stream's previous kernel, this call's other items, drains
 int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, bool early, cudaStream_t s) {
     if (it.count <= 0) return VIT_OK;
@@ -543,11 +588,7 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     int rc = run_items(a, 1, pn.seq, false, s);
     if (rc == VIT_OK) rc = run_items(a, 0, pn.prefix, pn.seq.count > 0, s);
     if (rc != VIT_OK || pn.p.parts == 1) return rc;
-    const unsigned grid = static_cast<unsigned>((int64_t(d.n_seq) * d.max_q * d.n_heads + 7) / 8);
-    const cudaError_t e = d.dtype == VIT_DTYPE_BF16
-                              ? launch_pdl(vitk::prefix_join_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, s, 1, a)
-                              : launch_pdl(vitk::prefix_join_kernel<__half>, dim3(grid), dim3(256), 0, s, 1, a);
-    return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
+    return d.dtype == VIT_DTYPE_BF16 ? join<__nv_bfloat16>(a, s) : join<__half>(a, s);
 }
 
 }  // namespace vith

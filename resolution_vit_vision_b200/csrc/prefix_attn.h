@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "../../include/vit.h"
 #include "../../include/vit_decoder.h"
 
 namespace vitk {
@@ -55,7 +56,7 @@ __device__ __forceinline__ SeqRange seq_range(const prefix_attention_desc &d, in
         a = static_cast<int64_t>(b) * d.max_q;
         e = a + d.max_q;
     }
-    r.ok = a >= 0 && e >= a && e <= d.total_q && e - a <= d.max_q;
+    r.ok = a >= 0 && e >= a && e <= d.total_q && e - a <= d.max_q && (b > 0 || a == 0);
     r.q0 = a < 0 ? 0 : (a > d.total_q ? d.total_q : a);
     int64_t n = (e > d.total_q ? d.total_q : e) - r.q0;
     n = n < 0 ? 0 : (n > d.max_q ? d.max_q : n);
@@ -64,6 +65,13 @@ __device__ __forceinline__ SeqRange seq_range(const prefix_attention_desc &d, in
     r.ok = r.ok && len >= 0 && len <= d.max_len;
     r.len = static_cast<int>(len < 0 ? 0 : (len > d.max_len ? d.max_len : len));
     return r;
+}
+
+// Where no item belongs to a sequence (a prefix alone), the first CTA checks the query ranges.
+__device__ __forceinline__ void check_ranges(const PrefixArgs &a) {
+    if (blockIdx.x != 0 || a.p.seq_splits != 0 || a.status == nullptr || a.d.cu_q == nullptr) return;
+    for (int b = threadIdx.x; b < a.d.n_seq; b += blockDim.x)
+        if (!seq_range(a.d, b).ok) atomicExch(a.status, VIT_ERR_LIMIT);
 }
 
 }  // namespace vitk

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int n_q, len = 0, b = 0, part, row0, t0, t1, n_prefix_tiles, own_keys = 0;
     const int prefix_tiles = static_cast<int>((d.prefix_len + kTcNK - 1) / kTcNK);
     if (kind == 0) {
+        check_ranges(a);
         part = rest % pl.prefix_splits;
         row0 = rest / pl.prefix_splits * vith::kTcRows;
         q0 = 0;

@@ -89,9 +89,10 @@ def test_several_queries_each(n_q):
 
 
 @pytest.mark.parametrize("Lp", [0, 3])
-def test_rows_without_keys(Lp):
+@pytest.mark.parametrize("n_q, lens", [([5, 4, 2], [2, 0, 0]), ([200, 131, 3], [100, 0, 2])])
+def test_rows_without_keys(n_q, lens, Lp):
     # more queries than own keys: the first rows see the prefix only, or nothing
-    a, cu = _case(7, 3, [5, 4, 2], [2, 0, 0], Lp, 4, 2, 64, "bf16", cap=9)
+    a, cu = _case(7, 3, n_q, lens, Lp, 4, 2, 64, "bf16", cap=109)
     _check(a, cu, nv.prefix_attention(**a))
 
 
@@ -179,6 +180,54 @@ def test_bad_lengths_are_flagged_and_stay_inside():
         torch.cuda.synchronize()
         assert st.item() == nv.VIT_ERR_LIMIT, bad
         assert torch.equal(got[0][:1], good[0][:1])      # row 1 is named twice by the first of them
+
+
+def test_bad_query_ranges_of_a_prefix_alone():
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    a, cu = _case(15, 3, [2, 3, 2], None, 40, 4, 2, 64, "bf16")
+    good = nv.prefix_attention(**a, status=st)
+    assert st.item() == 0
+    for bad in ([0, 2, 1, 3], [1, 2, 5, 7], [0, 2, 5, 9]):
+        st.zero_()
+        nv.prefix_attention(**dict(a, cu_q=torch.tensor(bad, dtype=torch.int32, device=DEV)), status=st)
+        assert st.item() == nv.VIT_ERR_LIMIT, bad
+    again = nv.prefix_attention(**a)
+    assert torch.equal(again[0], good[0])
+
+
+@pytest.mark.parametrize("n_q", [1, 150])
+def test_offsets_beyond_32_bits(n_q):
+    # sequences 2^32 + 64 bytes apart in the keys' cache and 2^31 elements + 64 in the values'
+    a, cu = _case(34, 2, n_q, [n_q + 30, n_q + 77], 70, 4, 2, 64, "bf16")
+    want = nv.prefix_attention(**a)
+    far = dict(a)
+    for n, seq in (("k", (1 << 31) + 64), ("v", (1 << 31) + (1 << 30))):
+        store = torch.empty(seq + a[n][0].numel(), dtype=torch.bfloat16, device=DEV)
+        far[n] = store.as_strided(a[n].shape, (seq,) + a[n].stride()[1:])
+        far[n].copy_(a[n])
+    got = nv.prefix_attention(**far)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_calls_on_two_streams_at_once():
+    a, cu = _case(35, 5, 2, [30, 60, 64, 100, 7], 900, 14, 2, 128, "bf16")
+    b, _ = _case(36, 40, 1, [1 + 3 * i for i in range(40)], 700, 28, 4, 128, "bf16")
+    want_a, want_b = nv.prefix_attention(**a), nv.prefix_attention(**b)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [(nv.prefix_attention(**a, stream=s), nv.prefix_attention(**b, stream=t)) for _ in range(10)]
+    torch.cuda.synchronize()
+    for ga, gb in got:
+        assert torch.equal(ga[0], want_a[0]) and torch.equal(gb[0], want_b[0])
+
+
+def test_wrong_stream_device_is_refused():
+    a, _ = _case(37, 1, 1, [3], 5, 4, 2, 64, "bf16")
+
+    class Elsewhere:
+        device = torch.device("cuda", 77)
+    with pytest.raises(ValueError):
+        nv.prefix_attention(**a, stream=Elsewhere())
 
 
 def test_lengths_read_by_a_replayed_graph():
