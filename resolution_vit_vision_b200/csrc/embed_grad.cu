@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     embed_sort_kernel(const int32_t *__restrict__ ids, int L, int64_t vocab, int64_t n_vision, int passes, bool mark,
                       EmbedWs ws, uint4 *__restrict__ zeros, int64_t n_zeros, int32_t *status) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();                                             // the next launches start early and wait
     if (blockIdx.x >= CTAS) {                                  // not the sorting cluster: zeros
         const int64_t stride = static_cast<int64_t>(gridDim.x - CTAS) * kSortThreads;
 #pragma unroll 4
@@ -313,6 +314,8 @@ __device__ __forceinline__ void zero_rows(const EmbedReduceArgs &a, int64_t r0, 
 template <typename T, typename G>
 __global__ void __launch_bounds__(kReduceThreads) embed_reduce_kernel(const __grid_constant__ EmbedReduceArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
+    pdl_wait();                                               // sorted
     const int n_text = a.head[0];
     if (blockIdx.x < a.sum_ctas) {                            // ---- a chunk's runs
         __shared__ uint32_t s_key[kMaxChunk + 2];             // entries c0 - 1 .. c0 + n
@@ -391,6 +394,7 @@ constexpr int kJoinThreads = 256, kJoinCols = 256, kJoinGroups = kJoinThreads / 
 
 template <typename G>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(const __grid_constant__ EmbedReduceArgs a) {
+    pdl_wait();                                               // the partial rows are written
     if (blockIdx.x >= a.join_ctas) {
         zero_rows<G>(a, a.zero_to + static_cast<int64_t>(blockIdx.x - a.join_ctas) * kZeroRows, a.vocab);
         return;
@@ -519,14 +523,13 @@ cudaError_t sort(const int32_t *ids, int64_t L, int64_t vocab, int64_t n_vision,
 template <typename T, typename G>
 cudaError_t reduce(const vitk::EmbedReduceArgs &a, cudaStream_t s) {
     const int64_t grid = a.sum_ctas + a.vision_ctas + (a.zero_to - a.zero_from + vitk::kZeroRows - 1) / vitk::kZeroRows;
+    cudaError_t e = cudaSuccess;
     if (grid > 0)
-        vitk::embed_reduce_kernel<T, G><<<static_cast<unsigned>(grid), vitk::kReduceThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+        e = launch_pdl(vitk::embed_reduce_kernel<T, G>, dim3(static_cast<unsigned>(grid)), dim3(vitk::kReduceThreads), 0, s, 1, a);
     const int64_t rest = a.accumulate ? 0 : (a.vocab - a.zero_to + vitk::kZeroRows - 1) / vitk::kZeroRows;
-    if (e == cudaSuccess && a.join_ctas + rest > 0) {
-        vitk::embed_join_kernel<G><<<static_cast<unsigned>(a.join_ctas + rest), vitk::kJoinThreads, 0, s>>>(a);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && a.join_ctas + rest > 0)
+        e = launch_pdl(vitk::embed_join_kernel<G>, dim3(static_cast<unsigned>(a.join_ctas + rest)), dim3(vitk::kJoinThreads),
+                       0, s, 1, a);
     return e;
 }
 

@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_grad_kernel(const _
     const int g = lane % GL, slot = lane / GL;
     const bool lane_live = g * V < half;
     float *s_cos = s_cs[warp][0], *s_sin = s_cs[warp][1];
+    pdl_trigger();                      // the sums' launch may start early; it waits for this one
     uint4 *ring = s_ring + threadIdx.x;
     NormSteps now, ahead;
     now.init(a, static_cast<int64_t>(blockIdx.x) * kNormWarps + warp, static_cast<int64_t>(gridDim.x) * kNormWarps, kSlots);
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__
     const int c = threadIdx.x & 31, rg = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + c;
     float v = 0.f;
+    pdl_wait();   // the partials are written
     if (col < 2 * D) {
 #pragma unroll 8
         for (int p = rg; p < n_part; p += 32) v += part[static_cast<int64_t>(p) * 2 * D + col];
@@ -574,9 +576,9 @@ int norm_rope_grad_launch(const NormRopeCall &c, float *dqw, float *dkw, void *w
         if (e != cudaSuccess) return VIT_ERR_CUDA;
     }
     if (dqw || dkw) {   // no tokens: the sums over nothing are written as zeros
-        vitk::norm_dw_kernel<<<(2 * c.head_dim + 31) / 32, 1024, 0, s>>>(static_cast<const float *>(workspace),
-                                                                         static_cast<int>(grid), c.head_dim, dqw, dkw);
-        if (cudaGetLastError() != cudaSuccess) return VIT_ERR_CUDA;
+        if (launch_pdl(vitk::norm_dw_kernel, dim3((2 * c.head_dim + 31) / 32), dim3(1024), 0, s, 1,
+                       static_cast<const float *>(workspace), static_cast<int>(grid), c.head_dim, dqw, dkw) != cudaSuccess)
+            return VIT_ERR_CUDA;
     }
     return VIT_OK;
 }
