@@ -7,11 +7,11 @@
 // o = sum_j w_j o_j / sum_j w_j, w_j = exp(lse_j - max lse). Hence the prefix part can be computed for
 // the stacked queries of the whole batch, its K and V read once for all of them.
 //
-//   prefix_small_kernel   row tiles of 16 or 64 query rows (a row is a token and one of the G query
+//   prefix_small_kernel   row tiles of 16 or 32 query rows (a row is a token and one of the G query
 //                         heads of a key-value head, so G x tokens rows share every key), keys in
 //                         tiles of 64 through a 3-deep cp.async ring, m16n8k16 tensor-core products
-//                         with fp32 sums; with 16 rows the four warps take a quarter of each key tile
-//                         and join at the end. Rows of few queries are bound by reading K and V from
+//                         with fp32 sums; the four warps take a quarter (or, with 32 rows, half) of each
+//                         key tile and join at the end. Rows of few queries are bound by reading K and V from
 //                         HBM: the products of a 16-row tile need about a fifth of the time its keys
 //                         take to arrive, so the wider tensor-core path would idle.
 //   prefix_join_kernel    one warp per (token, head): joins the parts.
@@ -28,7 +28,8 @@ namespace vitk {
 
 constexpr int kSmThreads = 128, kSmKeys = 64;
 // Ring depth and CTAs per SM: items of 16 rows are short and wait for their lengths and first keys, so
-// three CTAs with two stages each beat two with three (measured below); 64 rows need the registers.
+// three CTAs with two stages each take them (as fast as two with three on 64 sequences, 1% faster on 256);
+// 32 rows need the registers.
 template <int WR>
 constexpr int kSmStages = WR == 1 ? 2 : 3;
 template <int WR>
@@ -441,7 +442,7 @@ cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, boo
 
 template <typename T, int DP>
 cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool early, cudaStream_t s) {
-    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, early, s) : launch_small<T, DP, 4, 1>(a, kind, items, early, s);
+    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, early, s) : launch_small<T, DP, 2, 2>(a, kind, items, early, s);
 }
 
 template <typename T>
@@ -453,50 +454,52 @@ cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, boo
 
 // One kind of work item: which kernel takes it and how its keys are cut.
 struct Items {
-    int m = 0;              // query rows per item: 16 or 64 (small kernel), kTcRows (tensor-core kernel)
+    int m = 0;              // query rows per item: 16 or 32 (small kernel), kTcRows (tensor-core kernel)
     int keys = 0;           // keys per tile
     int splits = 0;         // parts of the keys
     int tiles_per_split = 0;
     int64_t count = 0;
+    double us = 0;          // the time expected for them
 };
 
-// Up to 64 rows the small kernel: below that its tiles are as fast as their keys arrive (a 64-key tile of
-// 128 dims is 32 KB, 1.5 us of a CTA's share of HBM), the tensor-core kernel would run its 128-row tiles
-// mostly empty.
-Items shape(int64_t rows) {
+// The items of `rows` query rows per key-value head in each of `runs` runs, whose keys are `shared` ones that
+// every item has and up to `own` ones of a sequence's. Up to 32 rows the small kernel: its tiles are as fast
+// as their keys arrive, and the tensor-core kernel would run 128-row tiles mostly empty (28 rows, 4113
+// shared keys: 18.6 us a call against 19.3; 63 rows in each of 16 sequences: 27.6 us on the tensor cores
+// against 31.6 in small tiles of 64 rows).
+// The keys are cut into parts so that the waves of resident CTAs fill up, against what the parts cost: every
+// part writes and the join reads an fp32 row of o.
+Items items(int64_t rows, int64_t runs, int64_t shared, int64_t own, int head_dim, int64_t part_row_bytes, bool joined) {
     Items it;
-    it.m = rows <= 16 ? 16 : rows <= 64 ? 64 : kTcRows;
-    it.keys = it.m == kTcRows ? kTcKeys : vitk::kSmKeys;
-    return it;
-}
-
-// Cuts the keys of `base` items of `tiles` tiles each so that the waves of CTAs (one per SM of the
-// tensor-core kernel, two of the small one) fill up, against what the parts cost: with more than one, every part writes
-// and the join reads an fp32 row of o, and the join is one more launch (about 4 us).
-void cut(Items &it, int64_t base, int tiles, int64_t part_row_bytes, bool joined, bool even, int max_splits) {
+    it.m = rows <= 16 ? 16 : rows <= 32 ? 32 : kTcRows;
     const bool tc = it.m == kTcRows;
-    const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;
-    const int64_t wave = tc ? 148 : it.m == 16 ? 148 * vitk::kSmCtas<1> : 148 * vitk::kSmCtas<4>;
-    double best = 1e30;
-    int pick = 1;
-    for (int s = 1; s <= std::min(tiles, max_splits); ++s) {
+    it.keys = tc ? kTcKeys : vitk::kSmKeys;
+    const int64_t base = runs * ceil_div(rows, it.m);
+    const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;           // measured, latency of one item
+    const int64_t wave = tc ? 148 : it.m == 16 ? 148 * vitk::kSmCtas<1> : 148 * vitk::kSmCtas<2>;
+    const int tiles = ceil_div(shared + own, it.keys);
+    // small items are bound together by what the L2 gives the SMs, 5 MB per us; own keys count 0.6 of their bound
+    const double stream_us = tc ? 0 : base * (shared + 0.6 * own) * head_dim * 4 / 5.0e6;
+    it.us = 1e30;
+    for (int s = 1; s <= std::max(1, std::min(tiles, 64)); ++s) {
         const int per = ceil_div(tiles, s);
         if (s > 1 && ceil_div(tiles, per) != s) continue;      // the same parts as a smaller s
-        // equal items of the prefix come in whole waves; a sequence's items differ in length, so the last
-        // one to start, which may be a long one, runs on behind an even share of the rest
+        // equal items come in whole waves; items of different lengths share the rest out, and the last one to
+        // start, which may be a long one, runs on
         const double item = per * tile_us + start_us;
-        double us = even ? item * static_cast<double>((base * s + wave - 1) / wave)
-                         : item * (1.0 + 0.6 * std::max(0.0, static_cast<double>(base * s) / wave - 1.0));
+        double us = own == 0 ? item * static_cast<double>((base * s + wave - 1) / wave)
+                             : item * (1.0 + 0.6 * std::max(0.0, static_cast<double>(base * s) / wave - 1.0));
+        us = std::max(us, stream_us);
         if (joined || s > 1) us += s * part_row_bytes * 2 / 4.0e6;
-        if (!joined && s > 1) us += 4.0;
-        if (us < best * 0.98) {
-            best = us;
-            pick = s;
+        if (!joined && s > 1) us += 4.0;                       // the join's launch
+        if (us < it.us * 0.98) {
+            it.us = us;
+            it.splits = s;
         }
     }
-    it.splits = pick;
-    it.tiles_per_split = ceil_div(std::max(tiles, 1), pick);
-    it.count = base * pick;
+    it.tiles_per_split = ceil_div(std::max(tiles, 1), it.splits);
+    it.count = base * it.splits;
+    return it;
 }
 
 struct Plan {
@@ -509,30 +512,28 @@ Plan make_plan(const prefix_attention_desc &d) {
     Plan pn{};
     vitk::PrefixPlan &p = pn.p;
     p.G = d.n_heads / d.n_kv_heads;
-    const bool own = d.k != nullptr && d.max_len > 0;
-    const int64_t max_rows = d.max_q * p.G, rows = d.total_q * p.G;
-    const int64_t part_row_bytes = d.total_q * d.n_heads * d.head_dim * int64_t(sizeof(float));
-    // Stacked or not, in tiles of 256 rows x 80 keys: stacking reads the prefix once for rows of all
-    // sequences but leaves two parts per row to join, whose fp32 rows cost about 12 tiles per 256 rows.
-    const int64_t pre80 = ceil_div(d.prefix_len, kTcKeys), own80 = own ? ceil_div(d.max_len, kTcKeys) : 0;
-    const int64_t seq_tiles = d.n_seq * int64_t(ceil_div(ceil_div(rows, d.n_seq), kTcRows)), all_tiles = ceil_div(rows, kTcRows);
-    p.stacked = d.n_seq > 1 && d.prefix_len > 0 &&
-                all_tiles * pre80 + seq_tiles * own80 + 12 * all_tiles < seq_tiles * (pre80 + own80);
-    const bool two_kinds = p.stacked && own;
-    if (p.stacked) {
-        pn.prefix = shape(rows);
-        cut(pn.prefix, int64_t(d.n_kv_heads) * ceil_div(rows, pn.prefix.m), ceil_div(d.prefix_len, pn.prefix.keys),
-            part_row_bytes, two_kinds, true, 64);
-        p.prefix_splits = pn.prefix.splits;
-        p.prefix_tiles_per_split = pn.prefix.tiles_per_split;
+    const bool own_keys = d.k != nullptr && d.max_len > 0;
+    const int64_t max_rows = d.max_q * p.G, rows = d.total_q * p.G, runs = int64_t(d.n_seq) * d.n_kv_heads;
+    const int64_t part_row_bytes = d.total_q * d.n_heads * d.head_dim * int64_t(sizeof(float)), own = own_keys ? d.max_len : 0;
+    // Every sequence's items over its prefix and own keys, or the prefix for the stacked rows of all sequences
+    // and each one's own keys apart: fewer tiles, but two launches more and two parts per row to join (64
+    // sequences, 64 shared and up to 200 own keys: 14.5 us a call against 24.6; 18 sequences, 4113 and 100: 42.8
+    // against 23.5).
+    pn.seq = items(max_rows, runs, d.prefix_len, own, d.head_dim, part_row_bytes, false);
+    if (d.n_seq > 1 && d.prefix_len > 0) {
+        const Items prefix = items(rows, d.n_kv_heads, d.prefix_len, 0, d.head_dim, part_row_bytes, own_keys);
+        Items apart;
+        if (own_keys) apart = items(max_rows, runs, 0, own, d.head_dim, part_row_bytes, true);
+        if (prefix.us + apart.us + (own_keys ? 4.0 : 0.0) < pn.seq.us) {
+            p.stacked = true;
+            pn.prefix = prefix;
+            pn.seq = apart;
+            p.prefix_splits = prefix.splits;
+            p.prefix_tiles_per_split = prefix.tiles_per_split;
+        }
     }
-    if (!p.stacked || own) {
-        pn.seq = shape(max_rows);
-        const int tiles = (own ? ceil_div(d.max_len, pn.seq.keys) : 0) + (p.stacked ? 0 : ceil_div(d.prefix_len, pn.seq.keys));
-        cut(pn.seq, int64_t(d.n_seq) * d.n_kv_heads * ceil_div(max_rows, pn.seq.m), tiles, part_row_bytes, two_kinds, false, 64);
-        p.seq_splits = pn.seq.splits;
-        p.min_tiles = pn.seq.splits > 1 ? 2 : 1;
-    }
+    p.seq_splits = pn.seq.splits;
+    p.min_tiles = pn.seq.splits > 1 ? 2 : 1;
     p.parts = p.prefix_splits + p.seq_splits;
     if (p.parts > 1) {
         pn.lse_bytes = (size_t(p.parts) * d.total_q * d.n_heads * sizeof(float) + 15) / 16 * 16;
