@@ -14,7 +14,9 @@
 //                         key tile and join at the end. Rows of few queries are bound by reading K and V from
 //                         HBM: the products of a 16-row tile need about a fifth of the time its keys
 //                         take to arrive, so the wider tensor-core path would idle.
-//   prefix_join_kernel    one warp per (token, head): joins the parts.
+//                         The parts of an item may be the CTAs of a cluster, which join in its shared
+//                         memory: for one or two short sequences a second launch is a third of the call.
+//   prefix_join_kernel    joins the parts that went through HBM, a warp or more per (token, head).
 // Statistics and sums are fp32; P is rounded to the element type for the P V product (weights at most
 // 1: the error of o is half an element step of max |v|), o is rounded once at the end.
 #include <algorithm>
@@ -93,24 +95,24 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
     pdl_trigger();
 
     // ---- the item: rows [row0, row0 + rows) of a run of queries, key tiles [t0, t1) of its list
-    const int h = blockIdx.x % d.n_kv_heads;
-    int rest = blockIdx.x / d.n_kv_heads;
+    const int splits = kind == 0 ? pl.prefix_splits : pl.seq_splits, split = blockIdx.x % splits;
+    int rest = blockIdx.x / splits;
+    const int h = rest % d.n_kv_heads;
+    rest /= d.n_kv_heads;
     int64_t q0;                                   // first token of the run
     int n_q, len = 0, b = 0, part;
     int row0, t0, t1, n_prefix_tiles, own_keys = 0;
     const int prefix_tiles = static_cast<int>((d.prefix_len + kSmKeys - 1) / kSmKeys);
     if (kind == 0) {
         check_ranges(a);
-        part = rest % pl.prefix_splits;
-        row0 = rest / pl.prefix_splits * M;
+        part = split;
+        row0 = rest * M;
         q0 = 0;
         n_q = static_cast<int>(d.total_q);
         n_prefix_tiles = prefix_tiles;
         t0 = part * pl.prefix_tiles_per_split;
         t1 = min(prefix_tiles, t0 + pl.prefix_tiles_per_split);
     } else {
-        const int sp = rest % pl.seq_splits;
-        rest /= pl.seq_splits;
         const int row_tiles = static_cast<int>((d.max_q * G + M - 1) / M);
         row0 = rest % row_tiles * M;
         b = rest / row_tiles;
@@ -124,13 +126,13 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
             return;
         }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
-        part = pl.prefix_splits + sp;
+        part = pl.prefix_splits + split;
         // keys behind the last row's own position are seen by no row of this tile
         own_keys = len;
         if (d.causal) own_keys = max(0, min(len, len - n_q + min(n_q - 1, (row0 + M - 1) / G) + 1));
         const int total = n_prefix_tiles + (own_keys + kSmKeys - 1) / kSmKeys;
         const int per = max(pl.min_tiles, (total + pl.seq_splits - 1) / pl.seq_splits);
-        t0 = min(total, sp * per);
+        t0 = min(total, split * per);
         t1 = min(total, t0 + per);
     }
     const int rows = min(M, n_q * G - row0);
@@ -288,7 +290,6 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
     constexpr int kOP = DP + 4;                                // fp32 row pitch
     float *so = reinterpret_cast<float *>(sm);                 // [WK][M][kOP]
     float *sml = so + WK * M * kOP;                            // [WK][M][2]
-    static_assert((WK * M * kOP + 2 * WK * M) * 4 <= kSmSmem<DP, WR>, "epilogue fits in the ring");
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -306,6 +307,9 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
     __syncthreads();
     int64_t q_end = q0 + n_q;
     if (kind == 0 && d.cu_q != nullptr) q_end = d.cu_q[d.n_seq];   // rows behind the last sequence stay as they were
+    float *s_part = sml + 2 * WK * M;                          // [M][2]: maximum and sum of this CTA's part
+    static_assert((WK * M * kOP + 2 * WK * M + 2 * M) * 4 <= kSmSmem<DP, WR>, "epilogue fits in the ring");
+    // words of 8 dims of a row: this CTA's part
     for (int i = tid; i < rows * (DP / 8); i += kSmThreads) {
         const int r = i / (DP / 8), c = i % (DP / 8) * 8;
         if (c >= D) continue;
@@ -322,12 +326,22 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += p[e] * f;
         }
+        const int64_t token = token_of(r);
+        const int head = head_of(r);
+        if (pl.cluster && kind == 1) {                         // left in place of the first key group's
+            float4 *p = reinterpret_cast<float4 *>(so + r * kOP + c);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (c == 0) {
+                s_part[2 * r] = mm;
+                s_part[2 * r + 1] = ll;
+            }
+            continue;
+        }
         const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= inv;
         const float lse2 = off + log2f(ll);                   // -inf where no key was visible
-        const int64_t token = token_of(r);
-        const int head = head_of(r);
         if (pl.parts == 1) {
             if (token >= q_end) continue;
             *reinterpret_cast<uint4 *>(static_cast<T *>(d.out) + token * d.out_stride + head * D + c) = Vec<T>::pack(v);
@@ -339,6 +353,41 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
             if (c == 0) pl.part_lse[row] = lse2;
         }
+    }
+    if (pl.cluster && kind == 1) {
+        cluster_sync();
+        // each CTA joins every splits-th word over all CTAs' parts
+        for (int i = tid * splits + split; i < rows * (DP / 8); i += kSmThreads * splits) {
+            const int r = i / (DP / 8), c = i % (DP / 8) * 8;
+            if (c >= D) continue;
+            float mm = -INFINITY;
+            for (int p = 0; p < splits; ++p) mm = fmaxf(mm, ld_cluster_f2(cluster_addr(s_part + 2 * r, p)).x);
+            const float off = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int p = 0; p < splits; ++p) {
+                const float2 ml = ld_cluster_f2(cluster_addr(s_part + 2 * r, p));
+                const uint32_t at = cluster_addr(so + r * kOP + c, p);
+                const float4 a0 = ld_cluster_f4(at), a1 = ld_cluster_f4(at + 16);
+                const float f = exp2_mufu(ml.x - off);
+                ll += ml.y * f;
+                v[0] += a0.x * f;
+                v[1] += a0.y * f;
+                v[2] += a0.z * f;
+                v[3] += a0.w * f;
+                v[4] += a1.x * f;
+                v[5] += a1.y * f;
+                v[6] += a1.z * f;
+                v[7] += a1.w * f;
+            }
+            const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= inv;
+            const int64_t token = token_of(r);
+            const int head = head_of(r);
+            *reinterpret_cast<uint4 *>(static_cast<T *>(d.out) + token * d.out_stride + head * D + c) = Vec<T>::pack(v);
+            if (c == 0 && d.lse) d.lse[token * d.n_heads + head] = (off + log2f(ll)) * kLn2;
+        }
+        cluster_sync();                                        // the others may still be reading this CTA's part
     }
     pdl_wait();   // done only when the launch before is: the join waits for the last one alone
 }
@@ -432,12 +481,26 @@ cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, boo
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
-    if (early)
-        return launch_pdl(vitk::prefix_small_kernel<T, DP, WR, WK>, dim3(static_cast<unsigned>(items)),
-                          dim3(vitk::kSmThreads), vitk::kSmSmem<DP, WR>, s, 1, a, kind);
-    vitk::prefix_small_kernel<T, DP, WR, WK>
-        <<<static_cast<unsigned>(items), vitk::kSmThreads, vitk::kSmSmem<DP, WR>, s>>>(a, kind);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[2];
+    int n_attr = 0;
+    if (early) {
+        attr[n_attr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n_attr++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (kind == 1 && a.p.cluster) {
+        attr[n_attr].id = cudaLaunchAttributeClusterDimension;
+        attr[n_attr].val.clusterDim.x = static_cast<unsigned>(a.p.seq_splits);
+        attr[n_attr].val.clusterDim.y = attr[n_attr].val.clusterDim.z = 1;
+        ++n_attr;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(items));
+    cfg.blockDim = dim3(vitk::kSmThreads);
+    cfg.dynamicSmemBytes = vitk::kSmSmem<DP, WR>;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = static_cast<unsigned>(n_attr);
+    return cudaLaunchKernelEx(&cfg, vitk::prefix_small_kernel<T, DP, WR, WK>, a, kind);
 }
 
 template <typename T, int DP>
@@ -452,6 +515,8 @@ cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, boo
     return small<T, 128>(a, kind, m, items, early, s);
 }
 
+constexpr int kMaxCluster = 8;            // the portable cluster size
+
 // One kind of work item: which kernel takes it and how its keys are cut.
 struct Items {
     int m = 0;              // query rows per item: 16 or 32 (small kernel), kTcRows (tensor-core kernel)
@@ -459,6 +524,7 @@ struct Items {
     int splits = 0;         // parts of the keys
     int tiles_per_split = 0;
     int64_t count = 0;
+    bool cluster = false;   // the parts of an item join in the shared memory of a cluster of CTAs
     double us = 0;          // the time expected for them
 };
 
@@ -490,11 +556,16 @@ Items items(int64_t rows, int64_t runs, int64_t shared, int64_t own, int head_di
         double us = own == 0 ? item * static_cast<double>((base * s + wave - 1) / wave)
                              : item * (1.0 + 0.6 * std::max(0.0, static_cast<double>(base * s) / wave - 1.0));
         us = std::max(us, stream_us);
-        if (joined || s > 1) us += s * part_row_bytes * 2 / 4.0e6;
-        if (!joined && s > 1) us += 4.0;                       // the join's launch
+        // up to eight short parts of small items join in a cluster's shared memory, with no part in HBM and no
+        // launch (one sequence, 265 shared keys: 10.2 -> 8.2 us); parts of nine tiles in clusters lost to more of
+        // them and a join (4 sequences, 4113 shared keys: 22.5 us against 18.5)
+        const bool cluster = !joined && !tc && own > 0 && s > 1 && s <= kMaxCluster && per <= 4;
+        if (joined || (s > 1 && !cluster)) us += s * part_row_bytes * 2 / 4.0e6;
+        if (!joined && s > 1) us += cluster ? 1.0 : 4.0;       // the meeting, or the join's launch
         if (us < it.us * 0.98) {
             it.us = us;
             it.splits = s;
+            it.cluster = cluster;
         }
     }
     it.tiles_per_split = ceil_div(std::max(tiles, 1), it.splits);
@@ -533,8 +604,9 @@ Plan make_plan(const prefix_attention_desc &d) {
         }
     }
     p.seq_splits = pn.seq.splits;
-    p.min_tiles = pn.seq.splits > 1 ? 2 : 1;
-    p.parts = p.prefix_splits + p.seq_splits;
+    p.min_tiles = pn.seq.splits > 1 && !pn.seq.cluster ? 2 : 1;
+    p.cluster = pn.seq.cluster;
+    p.parts = p.cluster ? 1 : p.prefix_splits + p.seq_splits;
     if (p.parts > 1) {
         pn.lse_bytes = (size_t(p.parts) * d.total_q * d.n_heads * sizeof(float) + 15) / 16 * 16;
         pn.o_bytes = size_t(p.parts) * part_row_bytes;

@@ -89,23 +89,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_trigger();
 
     // ---- the item (as prefix_small_kernel's)
-    const int h = blockIdx.x % d.n_kv_heads;
-    int rest = blockIdx.x / d.n_kv_heads;
+    const int splits = kind == 0 ? pl.prefix_splits : pl.seq_splits, split = blockIdx.x % splits;
+    int rest = blockIdx.x / splits;
+    const int h = rest % d.n_kv_heads;
+    rest /= d.n_kv_heads;
     int64_t q0;
     int n_q, len = 0, b = 0, part, row0, t0, t1, n_prefix_tiles, own_keys = 0;
     const int prefix_tiles = static_cast<int>((d.prefix_len + kTcNK - 1) / kTcNK);
     if (kind == 0) {
         check_ranges(a);
-        part = rest % pl.prefix_splits;
-        row0 = rest / pl.prefix_splits * vith::kTcRows;
+        part = split;
+        row0 = rest * vith::kTcRows;
         q0 = 0;
         n_q = static_cast<int>(d.total_q);
         n_prefix_tiles = prefix_tiles;
         t0 = part * pl.prefix_tiles_per_split;
         t1 = min(prefix_tiles, t0 + pl.prefix_tiles_per_split);
     } else {
-        const int sp = rest % pl.seq_splits;
-        rest /= pl.seq_splits;
         const int row_tiles = static_cast<int>((d.max_q * G + vith::kTcRows - 1) / vith::kTcRows);
         row0 = rest % row_tiles * vith::kTcRows;
         b = rest / row_tiles;
@@ -119,12 +119,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             return;
         }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
-        part = pl.prefix_splits + sp;
+        part = pl.prefix_splits + split;
         own_keys = len;
         if (d.causal) own_keys = max(0, min(len, len - n_q + min(n_q - 1, (row0 + vith::kTcRows - 1) / G) + 1));
         const int total = n_prefix_tiles + (own_keys + kTcNK - 1) / kTcNK;
         const int per = max(pl.min_tiles, (total + pl.seq_splits - 1) / pl.seq_splits);
-        t0 = min(total, sp * per);
+        t0 = min(total, split * per);
         t1 = min(total, t0 + per);
     }
     const int rows = min(vith::kTcRows, n_q * G - row0);
