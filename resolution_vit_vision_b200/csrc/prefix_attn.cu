@@ -133,9 +133,17 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
         own_keys = len;
         if (d.causal) own_keys = max(0, min(len, len - n_q + min(n_q - 1, (row0 + M - 1) / G) + 1));
         const int total = n_prefix_tiles + (own_keys + kSmKeys - 1) / kSmKeys;
-        const int per = max(pl.min_tiles, (total + pl.seq_splits - 1) / pl.seq_splits);
+        // a part has seq_tiles tiles (short sequences fill the first parts alone), a cluster shares evenly
+        const int per = pl.cluster ? (total + pl.seq_splits - 1) / pl.seq_splits : pl.seq_tiles;
         t0 = min(total, split * per);
         t1 = min(total, t0 + per);
+        if (t0 == t1 && pl.parts > 1) {        // a part without keys: its weight is 0, its o is not read
+            for (int r = tid; r < min(M, n_q * G - row0); r += kSmThreads)
+                pl.part_lse[(static_cast<int64_t>(part) * d.total_q + q0 + (row0 + r) / G) * d.n_heads + h * G + (row0 + r) % G] =
+                    -INFINITY;
+            pdl_wait();
+            return;
+        }
     }
     const int rows = min(M, n_q * G - row0);
     auto token_of = [&](int r) { return q0 + (row0 + r) / G; };
@@ -519,65 +527,66 @@ cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, boo
 
 constexpr int kMaxCluster = 8;            // the portable cluster size
 
-// One kind of work item: which kernel takes it and how its keys are cut.
-struct Items {
-    int m = 0;              // query rows per item: 16 or 32 (small kernel), kTcRows (tensor-core kernel)
-    int keys = 0;           // keys per tile
-    int splits = 0;         // parts of the keys
-    int tiles_per_split = 0;
-    int64_t count = 0;
-    bool cluster = false;   // the parts of an item join in the shared memory of a cluster of CTAs
-    double us = 0;          // the time expected for them
+// A way to cut the keys of an item: how many parts, of how many tiles, and the time expected of all items,
+// in us, without the join.
+struct Cut {
+    int splits, tiles;
+    double us;
 };
 
-// The items of `rows` query rows per key-value head in each of `runs` runs, whose keys are `shared` ones that
-// every item has and up to `own` ones of a sequence's. Up to 32 rows the small kernel: its tiles are as fast
-// as their keys arrive, and the tensor-core kernel would run 128-row tiles mostly empty (28 rows, 4113
-// shared keys: 18.6 us a call against 19.3; 63 rows in each of 16 sequences: 27.6 us on the tensor cores
-// against 31.6 in small tiles of 64 rows).
-// The keys are cut into parts so that the waves of resident CTAs fill up, against what the parts cost: every
-// part writes and the join reads an fp32 row of o.
-Items items(int64_t rows, int64_t runs, int64_t shared, int64_t own, int head_dim, int64_t part_row_bytes, bool joined) {
-    Items it;
-    it.m = rows <= 16 ? 16 : rows <= 32 ? 32 : kTcRows;
-    const bool tc = it.m == kTcRows;
-    it.keys = tc ? kTcKeys : vitk::kSmKeys;
-    const int64_t base = runs * ceil_div(rows, it.m);
+// One kind of work item: `rows` query rows per key-value head in each of `runs` runs, whose keys are `shared`
+// ones that every item has and up to `own` ones of a sequence's; which kernel takes it, and its cuts.
+struct Kind {
+    int m;                  // query rows per item: 16 or 32 (small kernel), kTcRows (tensor-core kernel)
+    int ctas;               // CTAs per SM
+    int64_t base;           // items before the cut
+    int n = 0;
+    Cut cut[40];
+    int64_t sms(const Cut &c) const { return std::min<int64_t>(148, (base * c.splits + ctas - 1) / ctas); }
+};
+
+// Up to 32 rows the small kernel: its tiles are as fast as their keys arrive, and the tensor-core kernel would
+// run 128-row tiles mostly empty (28 rows, 4113 shared keys: 18.6 us a call against 19.3; 63 rows in each of
+// 16 sequences: 27.6 us on the tensor cores against 31.6 in small tiles of 64 rows).
+Kind kind(int64_t rows, int64_t runs, int64_t shared, int64_t own, int head_dim) {
+    Kind k;
+    k.m = rows <= 16 ? 16 : rows <= 32 ? 32 : kTcRows;
+    const bool tc = k.m == kTcRows;
+    k.ctas = tc ? 1 : k.m == 16 ? vitk::kSmCtas<1> : vitk::kSmCtas<2>;
+    k.base = runs * ceil_div(rows, k.m);
     const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;           // measured, latency of one item
-    const int64_t wave = tc ? 148 : it.m == 16 ? 148 * vitk::kSmCtas<1> : 148 * vitk::kSmCtas<2>;
-    const int tiles = ceil_div(shared + own, it.keys);
+    const int64_t wave = 148 * k.ctas;
+    const int keys = tc ? kTcKeys : vitk::kSmKeys;
+    const int tiles = std::max(1, ceil_div(shared, keys) + ceil_div(own, keys));   // no tile holds keys of both
     // small items are bound together by what the L2 gives the SMs, 5 MB per us; own keys count 0.6 of their bound
-    const double stream_us = tc ? 0 : base * (shared + 0.6 * own) * head_dim * 4 / 5.0e6;
-    it.us = 1e30;
-    for (int s = 1; s <= std::max(1, std::min(tiles, 64)); ++s) {
+    const double stream_us = tc ? 0 : k.base * (shared + 0.6 * own) * head_dim * 4 / 5.0e6;
+    for (int s = 1; s <= 64 && k.n < 40;) {
         const int per = ceil_div(tiles, s);
-        if (s > 1 && ceil_div(tiles, per) != s) continue;      // the same parts as a smaller s
         // equal items come in whole waves; items of different lengths share the rest out, and the last one to
         // start, which may be a long one, runs on
-        const double item = per * tile_us + start_us;
-        double us = own == 0 ? item * static_cast<double>((base * s + wave - 1) / wave)
-                             : item * (1.0 + 0.6 * std::max(0.0, static_cast<double>(base * s) / wave - 1.0));
-        us = std::max(us, stream_us);
-        // up to eight short parts of small items join in a cluster's shared memory, with no part in HBM and no
-        // launch (one sequence, 265 shared keys: 10.2 -> 8.2 us); parts of nine tiles in clusters lost to more of
-        // them and a join (4 sequences, 4113 shared keys: 22.5 us against 18.5)
-        const bool cluster = !joined && !tc && own > 0 && s > 1 && s <= kMaxCluster && per <= 4;
-        if (joined || (s > 1 && !cluster)) us += s * part_row_bytes * 2 / 4.0e6;
-        if (!joined && s > 1) us += cluster ? 1.0 : 4.0;       // the meeting, or the join's launch
-        if (us < it.us * 0.98) {
-            it.us = us;
-            it.splits = s;
-            it.cluster = cluster;
-        }
+        const double item = per * tile_us + start_us, n = static_cast<double>(k.base) * s;
+        const double us = own == 0 ? item * static_cast<double>((k.base * s + wave - 1) / wave)
+                                   : item * (1.0 + 0.6 * std::max(0.0, n / wave - 1.0));
+        k.cut[k.n++] = Cut{s, per, std::max(us, stream_us)};
+        if (per == 1) break;
+        s = ceil_div(tiles, per - 1);                                           // the fewest parts of fewer tiles
     }
-    it.tiles_per_split = ceil_div(std::max(tiles, 1), it.splits);
-    it.count = base * it.splits;
-    return it;
+    return k;
 }
+
+struct Items {
+    int m = 0;
+    int splits = 0, tiles = 0;
+    int64_t count = 0;
+    double us = 0;
+    Items() = default;
+    Items(const Kind &k, const Cut &c) : m(k.m), splits(c.splits), tiles(c.tiles), count(k.base * c.splits), us(c.us) {}
+};
 
 struct Plan {
     vitk::PrefixPlan p;
     Items prefix, seq;
+    bool side_by_side;      // the SMs suffice for both kinds at once
     size_t o_bytes, lse_bytes;
 };
 
@@ -588,26 +597,64 @@ Plan make_plan(const prefix_attention_desc &d) {
     const bool own_keys = d.k != nullptr && d.max_len > 0;
     const int64_t max_rows = d.max_q * p.G, rows = d.total_q * p.G, runs = int64_t(d.n_seq) * d.n_kv_heads;
     const int64_t part_row_bytes = d.total_q * d.n_heads * d.head_dim * int64_t(sizeof(float)), own = own_keys ? d.max_len : 0;
-    // Every sequence's items over its prefix and own keys, or the prefix for the stacked rows of all sequences
-    // and each one's own keys apart: fewer tiles, but two launches more and two parts per row to join (64
-    // sequences, 64 shared and up to 200 own keys: 14.5 us a call against 24.6; 18 sequences, 4113 and 100: 42.8
-    // against 23.5).
-    pn.seq = items(max_rows, runs, d.prefix_len, own, d.head_dim, part_row_bytes, false);
-    if (d.n_seq > 1 && d.prefix_len > 0) {
-        const Items prefix = items(rows, d.n_kv_heads, d.prefix_len, 0, d.head_dim, part_row_bytes, own_keys);
-        Items apart;
-        if (own_keys) apart = items(max_rows, runs, 0, own, d.head_dim, part_row_bytes, true);
-        if (prefix.us + apart.us + (own_keys ? 4.0 : 0.0) < pn.seq.us) {
-            p.stacked = true;
-            pn.prefix = prefix;
-            pn.seq = apart;
-            p.prefix_splits = prefix.splits;
-            p.prefix_tiles_per_split = prefix.tiles_per_split;
+    // what a part costs (an fp32 row of o written and read, 4 MB per us) and the launch that joins them
+    const double part_us = part_row_bytes * 2 / 4.0e6, join_us = 4.0;
+    // Either every sequence's items go over its prefix and own keys in turn ...
+    const Kind all = kind(max_rows, runs, d.prefix_len, own, d.head_dim);
+    double best = 1e30;
+    for (int i = 0; i < all.n; ++i) {
+        const Cut &c = all.cut[i];
+        // up to eight short parts of small items join in a cluster's shared memory, with no part in HBM and no
+        // launch (one sequence, 265 shared keys: 10.2 -> 8.2 us); parts of nine tiles in clusters lost to more of
+        // them and a join (4 sequences, 4113 shared keys: 22.5 us against 18.5)
+        const bool cluster = all.m != kTcRows && own > 0 && c.splits > 1 && c.splits <= kMaxCluster && c.tiles <= 4;
+        const double us = c.us + (c.splits == 1 ? 0.0 : cluster ? 1.0 : c.splits * part_us + join_us);
+        if (us < best * 0.98) {
+            best = us;
+            pn.seq = Items(all, c);
+            p.cluster = cluster;
         }
     }
+    // ... or the prefix meets the stacked rows of all sequences, and each one's own keys its rows: fewer tiles, but
+    // more launches, and two parts or more per row to join (64 sequences, 64 shared and up to 200 own keys: 24.6 us
+    // a call against 14.5; 18 sequences, 4113 and 100: 23.5 against 42.8). The two kinds of items run side by side
+    // where the SMs suffice for both, else mostly one behind the other.
+    if (d.n_seq > 1 && d.prefix_len > 0) {
+        const Kind pre = kind(rows, d.n_kv_heads, d.prefix_len, 0, d.head_dim);
+        if (!own_keys) {
+            for (int i = 0; i < pre.n; ++i) {
+                const Cut &c = pre.cut[i];
+                const double us = c.us + (c.splits == 1 ? 0.0 : c.splits * part_us + join_us);
+                if (us < best * 0.98) {
+                    best = us;
+                    p.stacked = true;
+                    pn.prefix = Items(pre, c);
+                    pn.seq = Items();
+                }
+            }
+        } else {
+            const Kind seq = kind(max_rows, runs, 0, own, d.head_dim);
+            for (int i = 0; i < pre.n; ++i)
+                for (int j = 0; j < seq.n; ++j) {
+                    const Cut &c = pre.cut[i], &e = seq.cut[j];
+                    const double lo = std::min(c.us, e.us), hi = std::max(c.us, e.us);
+                    const double us = hi + (pre.sms(c) + seq.sms(e) <= 148 ? 0.0 : 0.75 * lo) +
+                                      (c.splits + e.splits) * part_us + join_us;
+                    if (us < best * 0.98) {
+                        best = us;
+                        p.stacked = true;
+                        pn.prefix = Items(pre, c);
+                        pn.seq = Items(seq, e);
+                        pn.side_by_side = pre.sms(c) + seq.sms(e) <= 148;
+                    }
+                }
+        }
+    }
+    p.cluster = p.cluster && !p.stacked;
+    p.prefix_splits = pn.prefix.splits;
+    p.prefix_tiles_per_split = pn.prefix.tiles;
     p.seq_splits = pn.seq.splits;
-    p.min_tiles = pn.seq.splits > 1 && !pn.seq.cluster ? 2 : 1;
-    p.cluster = pn.seq.cluster;
+    p.seq_tiles = pn.seq.tiles;
     p.parts = p.cluster ? 1 : p.prefix_splits + p.seq_splits;
     if (p.parts > 1) {
         pn.lse_bytes = (size_t(p.parts) * d.total_q * d.n_heads * sizeof(float) + 15) / 16 * 16;
@@ -658,12 +705,11 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     a.status = status;
     a.p.part_o = static_cast<float *>(workspace);
     a.p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pn.o_bytes);
-    // Which items start first (the others' launch fills the SMs they leave): the sequences' when the prefix's
-    // need most of the GPU, since they differ in length and the SMs that run out of them start on the
-    // prefix's, which are all alike (256 sequences: 118.6 us a call against 126.3); the prefix's when they are few,
-    // a whole SM each that they would have to wait for, and the others are quick (36 sequences of up to 100 own
-    // keys: 27.7 us against 30.0; with 64 of up to 517 the order costs 2 us of 38).
-    const bool prefix_first = pn.prefix.m == kTcRows && pn.prefix.count <= 100 && pn.seq.us < 0.5 * pn.prefix.us;
+    // Which items start first (the others' launch fills the SMs they leave): side by side the prefix's, a whole SM
+    // each that they would otherwise wait for (36 sequences of up to 100 own keys: 27.7 us against 30.0); one
+    // behind the other the sequences', since they differ in length and the SMs that run out of them start on the
+    // prefix's, which are all alike (256 sequences: 118.6 us against 126.3).
+    const bool prefix_first = pn.side_by_side;
     int rc = VIT_OK;
     for (int i = 0; i < 2 && rc == VIT_OK; ++i) {
         const bool early = i == 1 && pn.seq.count > 0 && pn.prefix.count > 0;

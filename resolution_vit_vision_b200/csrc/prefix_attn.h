@@ -27,7 +27,7 @@ struct PrefixPlan {
     int prefix_splits;       // stacked only: parts of the prefix, tiles_per_split key tiles each
     int prefix_tiles_per_split;
     int seq_splits;          // most parts of a sequence's own items (0: none, stacked without a suffix)
-    int min_tiles;           // fewest key tiles of a part of a sequence's items
+    int seq_tiles;           // key tiles of a part of a sequence's items
     bool cluster;            // the seq_splits CTAs of an item are a cluster and join in its shared memory
     int parts;               // prefix_splits + seq_splits, or 1 with clusters: what the join kernel joins
     float *part_o;           // fp32 [parts][total_q][n_heads][head_dim], unused with one part

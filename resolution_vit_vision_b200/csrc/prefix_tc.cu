@@ -126,9 +126,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         own_keys = len;
         if (d.causal) own_keys = max(0, min(len, len - n_q + min(n_q - 1, (row0 + vith::kTcRows - 1) / G) + 1));
         const int total = n_prefix_tiles + (own_keys + kTcNK - 1) / kTcNK;
-        const int per = max(pl.min_tiles, (total + pl.seq_splits - 1) / pl.seq_splits);
-        t0 = min(total, split * per);
-        t1 = min(total, t0 + per);
+        t0 = min(total, split * pl.seq_tiles);
+        t1 = min(total, t0 + pl.seq_tiles);
     }
     const int rows = min(vith::kTcRows, n_q * G - row0);
     const int n_kv = t1 - t0;
