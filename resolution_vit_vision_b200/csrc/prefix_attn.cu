@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
         n_q = r.n_q;
         len = r.len;
         if (row0 >= n_q * G) {
-            pdl_wait();
+            wait_for_launch_before();
             return;
         }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
             for (int r = tid; r < min(M, n_q * G - row0); r += kSmThreads)
                 pl.part_lse[(static_cast<int64_t>(part) * d.total_q + q0 + (row0 + r) / G) * d.n_heads + h * G + (row0 + r) % G] =
                     -INFINITY;
-            pdl_wait();
+            wait_for_launch_before();
             return;
         }
     }
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
         }
         cluster_sync();                                        // the others may still be reading this CTA's part
     }
-    pdl_wait();   // done only when the launch before is: the join waits for the last one alone
+    wait_for_launch_before();
 }
 
 // Joins the parts of a row (sequence, query, head): weights from the parts' lse, o in fp32, four dims per
@@ -527,11 +527,11 @@ cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, boo
 
 constexpr int kMaxCluster = 8;            // the portable cluster size
 
-// A way to cut the keys of an item: how many parts, of how many tiles, and the time expected of all items,
-// in us, without the join.
+// A way to cut the keys of an item: how many parts, of how many tiles, the time of one and that expected of
+// all on the whole GPU, in us, without the join.
 struct Cut {
     int splits, tiles;
-    double us;
+    double item, us;
 };
 
 // One kind of work item: `rows` query rows per key-value head in each of `runs` runs, whose keys are `shared`
@@ -540,9 +540,20 @@ struct Kind {
     int m;                  // query rows per item: 16 or 32 (small kernel), kTcRows (tensor-core kernel)
     int ctas;               // CTAs per SM
     int64_t base;           // items before the cut
+    bool even;              // items of one length
+    double stream_us;       // what bringing the keys in takes whatever the cut
     int n = 0;
     Cut cut[40];
     int64_t sms(const Cut &c) const { return std::min<int64_t>(148, (base * c.splits + ctas - 1) / ctas); }
+    // the time expected of all items on `sms` SMs: equal items come in whole waves; items of different lengths
+    // share the rest out, and the last one to start, which may be a long one, runs on
+    double us_on(const Cut &c, int64_t sms) const {
+        const int64_t n_items = base * c.splits, wave = sms * ctas;
+        const double waves = static_cast<double>(n_items) / wave;
+        return std::max(stream_us, even          ? c.item * static_cast<double>((n_items + wave - 1) / wave)
+                                   : waves > 1.0 ? c.item * (1.3 + 0.6 * (waves - 1.0))
+                                                 : c.item);
+    }
 };
 
 // Up to 32 rows the small kernel: its tiles are as fast as their keys arrive, and the tensor-core kernel would
@@ -555,19 +566,16 @@ Kind kind(int64_t rows, int64_t runs, int64_t shared, int64_t own, int head_dim)
     k.ctas = tc ? 1 : k.m == 16 ? vitk::kSmCtas<1> : vitk::kSmCtas<2>;
     k.base = runs * ceil_div(rows, k.m);
     const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;           // measured, latency of one item
-    const int64_t wave = 148 * k.ctas;
     const int keys = tc ? kTcKeys : vitk::kSmKeys;
     const int tiles = std::max(1, ceil_div(shared, keys) + ceil_div(own, keys));   // no tile holds keys of both
     // small items are bound together by what the L2 gives the SMs, 5 MB per us; own keys count 0.6 of their bound
-    const double stream_us = tc ? 0 : k.base * (shared + 0.6 * own) * head_dim * 4 / 5.0e6;
+    k.stream_us = tc ? 0 : k.base * (shared + 0.6 * own) * head_dim * 4 / 5.0e6;
+    k.even = own == 0;
     for (int s = 1; s <= 64 && k.n < 40;) {
         const int per = ceil_div(tiles, s);
-        // equal items come in whole waves; items of different lengths share the rest out, and the last one to
-        // start, which may be a long one, runs on
-        const double item = per * tile_us + start_us, n = static_cast<double>(k.base) * s;
-        const double us = own == 0 ? item * static_cast<double>((k.base * s + wave - 1) / wave)
-                                   : item * (1.0 + 0.6 * std::max(0.0, n / wave - 1.0));
-        k.cut[k.n++] = Cut{s, per, std::max(us, stream_us)};
+        k.cut[k.n] = Cut{s, per, per * tile_us + start_us, 0.0};
+        k.cut[k.n].us = k.us_on(k.cut[k.n], 148);
+        ++k.n;
         if (per == 1) break;
         s = ceil_div(tiles, per - 1);                                           // the fewest parts of fewer tiles
     }
@@ -586,7 +594,7 @@ struct Items {
 struct Plan {
     vitk::PrefixPlan p;
     Items prefix, seq;
-    bool side_by_side;      // the SMs suffice for both kinds at once
+    bool prefix_first;      // which launch comes first when there are two
     size_t o_bytes, lse_bytes;
 };
 
@@ -617,8 +625,9 @@ Plan make_plan(const prefix_attention_desc &d) {
     }
     // ... or the prefix meets the stacked rows of all sequences, and each one's own keys its rows: fewer tiles, but
     // more launches, and two parts or more per row to join (64 sequences, 64 shared and up to 200 own keys: 24.6 us
-    // a call against 14.5; 18 sequences, 4113 and 100: 23.5 against 42.8). The two kinds of items run side by side
-    // where the SMs suffice for both, else mostly one behind the other.
+    // a call against 14.5; 18 sequences, 4113 and 100: 23.5 against 42.8). The prefix's items may start first: they
+    // take a whole SM each, so the sequences' run beside them on the SMs that they leave, and on all when they are
+    // done. Or the sequences' start first, and the prefix's mostly come behind them.
     if (d.n_seq > 1 && d.prefix_len > 0) {
         const Kind pre = kind(rows, d.n_kv_heads, d.prefix_len, 0, d.head_dim);
         if (!own_keys) {
@@ -637,15 +646,20 @@ Plan make_plan(const prefix_attention_desc &d) {
             for (int i = 0; i < pre.n; ++i)
                 for (int j = 0; j < seq.n; ++j) {
                     const Cut &c = pre.cut[i], &e = seq.cut[j];
-                    const double lo = std::min(c.us, e.us), hi = std::max(c.us, e.us);
-                    const double us = hi + (pre.sms(c) + seq.sms(e) <= 148 ? 0.0 : 0.75 * lo) +
-                                      (c.splits + e.splits) * part_us + join_us;
+                    const int64_t left = 148 - pre.sms(c);
+                    double first = 1e30;
+                    if (left > 0) {
+                        const double beside = seq.us_on(e, left);
+                        first = beside <= c.us ? c.us : c.us + (1.0 - c.us / beside) * e.us;
+                    }
+                    const double behind = std::max(c.us, e.us) + 0.75 * std::min(c.us, e.us);
+                    const double us = std::min(first, behind) + (c.splits + e.splits) * part_us + join_us;
                     if (us < best * 0.98) {
                         best = us;
                         p.stacked = true;
                         pn.prefix = Items(pre, c);
                         pn.seq = Items(seq, e);
-                        pn.side_by_side = pre.sms(c) + seq.sms(e) <= 148;
+                        pn.prefix_first = first < behind;
                     }
                 }
         }
@@ -705,15 +719,12 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     a.status = status;
     a.p.part_o = static_cast<float *>(workspace);
     a.p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + pn.o_bytes);
-    // Which items start first (the others' launch fills the SMs they leave): side by side the prefix's, a whole SM
-    // each that they would otherwise wait for (36 sequences of up to 100 own keys: 27.7 us against 30.0); one
-    // behind the other the sequences', since they differ in length and the SMs that run out of them start on the
-    // prefix's, which are all alike (256 sequences: 118.6 us against 126.3).
-    const bool prefix_first = pn.side_by_side;
+    // the second launch starts early and fills the SMs that the first one leaves (36 sequences of up to 100 own
+    // keys: the prefix first 27.7 us, the sequences first 30.0)
     int rc = VIT_OK;
     for (int i = 0; i < 2 && rc == VIT_OK; ++i) {
         const bool early = i == 1 && pn.seq.count > 0 && pn.prefix.count > 0;
-        rc = (i == 0) == prefix_first ? run_items(a, 0, pn.prefix, early, s) : run_items(a, 1, pn.seq, early, s);
+        rc = (i == 0) == pn.prefix_first ? run_items(a, 0, pn.prefix, early, s) : run_items(a, 1, pn.seq, early, s);
     }
     if (rc != VIT_OK || pn.p.parts == 1) return rc;
     return d.dtype == VIT_DTYPE_BF16 ? join<__nv_bfloat16>(a, s) : join<__half>(a, s);

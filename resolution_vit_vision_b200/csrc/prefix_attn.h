@@ -7,6 +7,7 @@
 
 #include "../../include/vit.h"
 #include "../../include/vit_decoder.h"
+#include "ptx.cuh"
 
 namespace vitk {
 
@@ -66,6 +67,13 @@ __device__ __forceinline__ SeqRange seq_range(const prefix_attention_desc &d, in
     r.ok = r.ok && len >= 0 && len <= d.max_len;
     r.len = static_cast<int>(len < 0 ? 0 : (len > d.max_len ? d.max_len : len));
     return r;
+}
+
+// The join waits for the last launch of items alone, so that launch may not be done before the one that it
+// started beside. One CTA sees to it, the last: if all waited, the early ones would keep their SMs from the
+// rest until then (256 sequences beside the prefix: 122 us a call).
+__device__ __forceinline__ void wait_for_launch_before() {
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // Where no item belongs to a sequence (a prefix alone), the first CTA checks the query ranges.

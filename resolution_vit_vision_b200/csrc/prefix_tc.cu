@@ -64,7 +64,7 @@ template <typename T, int HV>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tpk, const __grid_constant__ CUtensorMap tpv,
                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                     const __grid_constant__ PrefixArgs a, int kind, int early) {
+                     const __grid_constant__ PrefixArgs a, int kind) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr int kQTile = HV * kTcQBox, kTile = HV * kTcKBox;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         n_q = r.n_q;
         len = r.len;
         if (row0 >= n_q * G) {
-            if (early) pdl_wait();
+            wait_for_launch_before();
             return;
         }
         n_prefix_tiles = pl.stacked ? 0 : prefix_tiles;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     }
 
-    if (early) pdl_wait();   // done only when the launch before is: the join waits for this kernel alone
+    wait_for_launch_before();
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) __nanosleep(200000);
@@ -476,9 +476,9 @@ cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kin
     }
     if (early)
         return launch_pdl(vitk::prefix_tc_kernel<T, HV>, dim3(static_cast<unsigned>(items)), dim3(vitk::kTcThreads),
-                          vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind, early ? 1 : 0);
+                          vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind);
     vitk::prefix_tc_kernel<T, HV><<<static_cast<unsigned>(items), vitk::kTcThreads, vitk::kTcSmem<HV>, s>>>(
-        m[0], m[1], m[2], m[3], a, kind, early ? 1 : 0);
+        m[0], m[1], m[2], m[3], a, kind);
     return cudaGetLastError();
 }
 
