@@ -126,8 +126,8 @@ typedef struct {
     void *out;                       /* as q, no overlap with any input                               */
     int64_t out_stride;
     float *lse;                      /* fp32 [total_q, n_heads] or NULL                               */
-    int64_t total_q;                 /* total_q * n_heads < 2^31                                      */
-    int64_t max_q;                   /* no sequence has more queries                                  */
+    int64_t total_q;                 /* total_q * n_heads <= 2^31 - 1024                              */
+    int64_t max_q;                   /* no sequence has more queries; max_q * n_seq * n_heads the same */
     const int32_t *cu_q;             /* [n_seq + 1] first row of each sequence's queries, from 0, or
                                         NULL: max_q each. Rows from cu_q[n_seq] on are left alone     */
     int n_seq;                       /* 1..65536                                                      */

@@ -876,8 +876,9 @@ int check_prefix(const prefix_attention_desc *d) {
         return VIT_ERR_ARG;
     if (d->n_seq > 65536 || d->n_heads > 65536 || d->prefix_len > (int64_t(1) << 30) || d->max_len > (int64_t(1) << 30))
         return VIT_ERR_LIMIT;
-    if (d->total_q > ((int64_t(1) << 31) - 1) / d->n_heads || d->max_q > ((int64_t(1) << 31) - 1) / d->n_heads / d->n_seq)
-        return VIT_ERR_LIMIT;
+    // rows of an item are numbered in 32 bits, up to a tile (256) behind the last
+    const int64_t most_rows = (int64_t(1) << 31) - 1024;
+    if (d->total_q > most_rows / d->n_heads || d->max_q > most_rows / d->n_heads / d->n_seq) return VIT_ERR_LIMIT;
     if (!d->cu_q && d->total_q != 0 && d->total_q != d->max_q * d->n_seq) return VIT_ERR_ARG;
     if (!d->k != !d->v || !d->k != !d->lens || (!d->k && d->max_len != 0)) return VIT_ERR_ARG;
     if (d->total_q > 0 && (!d->q || !d->out)) return VIT_ERR_ARG;

@@ -125,6 +125,17 @@ def test_prefix_attention_refusals(nv, bad, code):
     assert nv.lib().prefix_attention(ctypes.byref(d), P, 1 << 40, None, None) == getattr(nv, "VIT_ERR_" + code)
 
 
+def test_prefix_attention_row_numbers_fit(nv):
+    # an item's rows are numbered in 32 bits up to a tile behind the last: no row may come near 2^31
+    one = dict(n_heads=8, n_kv_heads=1, head_dim=8, q_stride=64, out_stride=64, cu_q=P.value, n_seq=1, k=None, v=None,
+               lens=None, max_len=0, max_q=1)
+    most = ((1 << 31) - 1024) // 8
+    for bad in (dict(total_q=most + 1), dict(total_q=6, max_q=most + 1), dict(total_q=6, n_seq=64, max_q=most // 64 + 1)):
+        d = _desc(nv, **{**one, **bad})
+        assert nv.lib().prefix_attention_workspace(ctypes.byref(d)) == 0
+        assert nv.lib().prefix_attention(ctypes.byref(d), P, 1 << 40, None, None) == nv.VIT_ERR_LIMIT
+
+
 def test_prefix_attention_workspace_is_checked(nv):
     d = _desc(nv, n_seq=100, total_q=200, prefix_len=5000)     # long enough for parts
     need = nv.lib().prefix_attention_workspace(ctypes.byref(d))
