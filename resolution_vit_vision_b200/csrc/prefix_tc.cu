@@ -435,7 +435,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     }
 
-    wait_for_launch_before();
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) __nanosleep(200000);
@@ -443,6 +442,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    // last of all: a CTA of the launch before might be waiting for this one's tensor memory
+    wait_for_launch_before();
 }
 
 }  // namespace vitk

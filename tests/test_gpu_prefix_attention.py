@@ -347,3 +347,18 @@ def test_dimensions_of_one_element_have_any_stride():
     b = dict(a, prefix_k=a["prefix_k"].as_strided((1, 1, 64), (1, 3, 1)), k=a["k"].as_strided((1, 1, 1, 64), (0, 7, 1, 1)))
     got = nv.prefix_attention(**b)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_prefix_and_sequences_on_the_tensor_cores_twice_at_once():
+    # both launches of a call take tensor memory, and the second starts beside the first; so do another stream's
+    cases = [_case(40 + i, 12, 200, [200 + 9 * b for b in range(12)], 2001, 12, 2, 64, "bf16") for i in range(2)]
+    streams = [torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = nv.prefix_attention(**cases[i][0])
+    torch.cuda.synchronize()
+    for (a, cu), g in zip(cases, got):
+        _check(a, cu, g)
