@@ -404,14 +404,15 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
 
 // Joins the parts of a row (sequence, query, head): weights from the parts' lse, o in fp32, four dims per
 // lane. W warps share a row, each with every W-th part, and meet in shared memory: a row of forty parts read
-// by one warp took 8 us of latency. Parts without keys were not written: they are read all the same (the
-// loads need not wait for the weights) and dropped by their weight of 0.
+// by one warp took 8 us of latency. Parts without keys were not written: they are read all the same (lse and o
+// come in one latency, the maximum runs along; the maximum first, then o cost 2 us a call) and dropped by their
+// weight of 0.
 constexpr int kJoinWarps = 8;
 
 template <typename T, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
     __shared__ float4 s_o[kJoinWarps][32];
-    __shared__ float s_w[kJoinWarps];
+    __shared__ float2 s_w[kJoinWarps];                         // maximum and sum of a warp's parts
     const prefix_attention_desc &d = a.d;
     const PrefixPlan &pl = a.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
@@ -425,43 +426,63 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     pdl_wait();   // the parts are written
     const int64_t token = r.q0 + j;
     const int64_t row = token * d.n_heads + head, pitch = d.total_q * d.n_heads;
-    float off = 0.f, sum = 0.f;
+    float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
-        float mx = -INFINITY;
-        for (int i = lane; i < pl.parts; i += 32) mx = fmaxf(mx, pl.part_lse[i * pitch + row]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        off = mx == -INFINITY ? 0.f : mx;
         const bool has = lane * 4 < d.head_dim;
-        const float *o = pl.part_o + row * d.head_dim + lane * 4;
-#pragma unroll 4
-        for (int i = sub; i < pl.parts; i += W) {
-            const float wt = exp2f(pl.part_lse[i * pitch + row] - off);
-            const float4 v = has ? *reinterpret_cast<const float4 *>(o + i * pitch * d.head_dim) : acc;
-            const bool use = wt != 0.f;
-            sum += wt;
-            acc.x += use ? wt * v.x : 0.f;
-            acc.y += use ? wt * v.y : 0.f;
-            acc.z += use ? wt * v.z : 0.f;
-            acc.w += use ? wt * v.w : 0.f;
+        const float *lse = pl.part_lse + row, *o = pl.part_o + row * d.head_dim + lane * 4;
+        for (int i0 = sub; i0 < pl.parts; i0 += 4 * W) {
+            float w[4];
+            float4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {                     // one latency for both: weights from a running maximum
+                const int i = i0 + u * W;
+                w[u] = -INFINITY;
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < pl.parts) {
+                    w[u] = lse[i * pitch];
+                    if (has) v[u] = *reinterpret_cast<const float4 *>(o + i * pitch * d.head_dim);
+                }
+            }
+            const float before = mx;
+            mx = fmaxf(mx, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
+            const float off = mx == -INFINITY ? 0.f : mx, f = exp2f(before - off);
+            sum *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float wt = exp2f(w[u] - off);
+                const bool use = wt != 0.f;
+                sum += wt;
+                acc.x += use ? wt * v[u].x : 0.f;
+                acc.y += use ? wt * v[u].y : 0.f;
+                acc.z += use ? wt * v[u].z : 0.f;
+                acc.w += use ? wt * v[u].w : 0.f;
+            }
         }
     }
     if (W > 1) {
         s_o[warp][lane] = acc;
-        if (lane == 0) s_w[warp] = sum;
+        if (lane == 0) s_w[warp] = make_float2(mx, sum);
         __syncthreads();
         if (sub != 0) return;
 #pragma unroll
-        for (int i = 1; i < W; ++i) {
+        for (int i = 1; i < W; ++i) mx = fmaxf(mx, s_w[warp + i].x);
+        const float off = mx == -INFINITY ? 0.f : mx;
+        sum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
             const float4 v = s_o[warp + i][lane];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
-            sum += s_w[warp + i];
+            const float f = exp2f(s_w[warp + i].x - off);
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+            sum += s_w[warp + i].y * f;
         }
     }
+    const float off = mx == -INFINITY ? 0.f : mx;
     if (!live) return;
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
     if (lane * 4 < d.head_dim)
