@@ -988,10 +988,7 @@ int prefix_attention(const prefix_attention_desc *desc, void *workspace, int64_t
                      void *stream) {
     const int rc = check_prefix(desc);
     if (rc != VIT_OK || desc->total_q == 0) return rc;
-    const int64_t need = vith::prefix_attention_bytes(*desc);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return VIT_ERR_ARG;
-    if (need > 0 && !aligned16(workspace)) return VIT_ERR_ALIGN;
-    return vith::prefix_attention_launch(*desc, workspace, dev_status, static_cast<cudaStream_t>(stream));
+    return vith::prefix_attention_launch(*desc, workspace, workspace_bytes, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 int vit_op_wait_selftest(int32_t *dev_status, int64_t limit_cycles, void *stream) {

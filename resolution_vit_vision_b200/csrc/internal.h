@@ -141,7 +141,8 @@ int64_t norm_rope_grad_workspace(int head_dim);
 int norm_rope_grad_launch(const NormRopeCall &c, float *dqw, float *dkw, void *workspace, cudaStream_t s);
 // ---- attention over a shared prefix (prefix_attn.cu)
 int64_t prefix_attention_bytes(const prefix_attention_desc &d);
-int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int32_t *status, cudaStream_t s);
+int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int64_t workspace_bytes, int32_t *status,
+                            cudaStream_t s);
 int wait_selftest_launch(int32_t *status, long long limit, cudaStream_t s);
 int mrope_launch(const int32_t *ids, int64_t L, const int32_t *grid_thw, int n_grids, int32_t *out, int32_t *delta,
                  int32_t *status, cudaStream_t s);

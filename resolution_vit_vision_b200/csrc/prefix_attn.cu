@@ -732,8 +732,12 @@ int64_t prefix_attention_bytes(const prefix_attention_desc &d) {
     return static_cast<int64_t>(pn.o_bytes + pn.lse_bytes);
 }
 
-int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int32_t *status, cudaStream_t s) {
-    const Plan pn = make_plan(d);
+int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int64_t workspace_bytes, int32_t *status,
+                            cudaStream_t s) {
+    const Plan pn = make_plan(d);              // 0.5 to 4 us of the host's time
+    const int64_t need = static_cast<int64_t>(pn.o_bytes + pn.lse_bytes);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return VIT_ERR_ARG;
+    if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16) return VIT_ERR_ALIGN;
     vitk::PrefixArgs a;
     a.d = d;
     a.p = pn.p;
