@@ -233,12 +233,14 @@ __global__ void __launch_bounds__(kNormThreads, 6) norm_rope_kernel(const __grid
     const int g = lane % GL, slot = lane / GL;
     const bool lane_live = g * V < half;
     float *s_cos = s_cs[warp][0], *s_sin = s_cs[warp][1];
+    pdl_trigger();
     uint4 *ring = s_ring + threadIdx.x;
     if (!lane_live)                                  // idle lanes add zeros to their group's sums
         for (int i = 0; i < 2 * kNormRing; ++i) ring[i * kNormThreads] = make_uint4(0, 0, 0, 0);
     NormSteps now, ahead;
     now.init(a, static_cast<int64_t>(blockIdx.x) * kNormWarps + warp, static_cast<int64_t>(gridDim.x) * kNormWarps, kSlots);
     ahead = now;
+    pdl_wait();                                      // what the stream did before is done
 #pragma unroll
     for (int i = 0; i < kNormRing - 1; ++i) {
         norm_fetch<T, 1>(a, ahead, ring + i * 2 * kNormThreads, slot, g * V, lane_live, half);
@@ -313,11 +315,12 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_grad_kernel(const _
     const int g = lane % GL, slot = lane / GL;
     const bool lane_live = g * V < half;
     float *s_cos = s_cs[warp][0], *s_sin = s_cs[warp][1];
-    pdl_trigger();                      // the sums' launch may start early; it waits for this one
+    pdl_trigger();                      // the next launch may start early; it waits for this one
     uint4 *ring = s_ring + threadIdx.x;
     NormSteps now, ahead;
     now.init(a, static_cast<int64_t>(blockIdx.x) * kNormWarps + warp, static_cast<int64_t>(gridDim.x) * kNormWarps, kSlots);
     ahead = now;
+    pdl_wait();                                      // what the stream did before is done
 #pragma unroll
     for (int i = 0; i < kNormGradRing - 1; ++i) {
         norm_fetch<T, 2>(a, ahead, ring + i * 4 * kNormThreads, slot, g * V, lane_live, half);
@@ -486,34 +489,36 @@ int token_share(int64_t L, int heads, int gl, int ctas) {
 
 template <typename T>
 cudaError_t forward(const vitk::NormRopeArgs &a, int gl, unsigned grid, cudaStream_t s) {
+    auto go = [&](auto *k) { return launch_pdl(k, dim3(grid), dim3(vitk::kNormThreads), vitk::kNormSmem, s, 1, a); };
     switch (gl) {
         case 1:   // 16 dims of a 16-bit type; 32-bit heads have two lanes or more
-            if constexpr (sizeof(T) == 2) vitk::norm_rope_kernel<T, 1><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a);
+            if constexpr (sizeof(T) == 2) return go(vitk::norm_rope_kernel<T, 1>);
             break;
-        case 2: vitk::norm_rope_kernel<T, 2><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
-        case 4: vitk::norm_rope_kernel<T, 4><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
-        case 8: vitk::norm_rope_kernel<T, 8><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
-        case 16: vitk::norm_rope_kernel<T, 16><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a); break;
+        case 2: return go(vitk::norm_rope_kernel<T, 2>);
+        case 4: return go(vitk::norm_rope_kernel<T, 4>);
+        case 8: return go(vitk::norm_rope_kernel<T, 8>);
+        case 16: return go(vitk::norm_rope_kernel<T, 16>);
         default:  // 32 lanes: fp32 heads of more than 128 dims
-            if constexpr (sizeof(T) == 4) vitk::norm_rope_kernel<T, 32><<<grid, vitk::kNormThreads, vitk::kNormSmem, s>>>(a);
+            if constexpr (sizeof(T) == 4) return go(vitk::norm_rope_kernel<T, 32>);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>
 cudaError_t backward(const vitk::NormRopeArgs &a, int gl, unsigned grid, cudaStream_t s) {
+    auto go = [&](auto *k) { return launch_pdl(k, dim3(grid), dim3(vitk::kNormThreads), vitk::kNormGradSmem, s, 1, a); };
     switch (gl) {
         case 1:   // 16 dims of a 16-bit type; 32-bit heads have two lanes or more
-            if constexpr (sizeof(T) == 2) vitk::norm_rope_grad_kernel<T, 1><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a);
+            if constexpr (sizeof(T) == 2) return go(vitk::norm_rope_grad_kernel<T, 1>);
             break;
-        case 2: vitk::norm_rope_grad_kernel<T, 2><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
-        case 4: vitk::norm_rope_grad_kernel<T, 4><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
-        case 8: vitk::norm_rope_grad_kernel<T, 8><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
-        case 16: vitk::norm_rope_grad_kernel<T, 16><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a); break;
+        case 2: return go(vitk::norm_rope_grad_kernel<T, 2>);
+        case 4: return go(vitk::norm_rope_grad_kernel<T, 4>);
+        case 8: return go(vitk::norm_rope_grad_kernel<T, 8>);
+        case 16: return go(vitk::norm_rope_grad_kernel<T, 16>);
         default:  // 32 lanes: fp32 heads of more than 128 dims
-            if constexpr (sizeof(T) == 4) vitk::norm_rope_grad_kernel<T, 32><<<grid, vitk::kNormThreads, vitk::kNormGradSmem, s>>>(a);
+            if constexpr (sizeof(T) == 4) return go(vitk::norm_rope_grad_kernel<T, 32>);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 void fill(vitk::NormRopeArgs &a, const NormRopeCall &c, int share) {

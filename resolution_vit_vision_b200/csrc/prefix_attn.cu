@@ -84,7 +84,7 @@ constexpr int kSmSmem = kSmStages<WR> * 2 * kSmTileBytes<DP> + (kSmStages<WR> ==
 // kind 0: items over the stacked queries and the prefix; 1: a sequence's items over its own keys
 // (stacked plan) or over prefix and own keys (the other plan)
 template <typename T, int DP, int WR, int WK>
-__global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(const __grid_constant__ PrefixArgs a, int kind) {
+__global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(const __grid_constant__ PrefixArgs a, int kind, bool second) {
     static_assert(WR * WK == kSmThreads / 32, "four warps");
     constexpr int M = 16 * WR, KW = kSmKeys / WK, NT = KW / 8, DT = DP / 8, KS = DP / 16;
     constexpr int kRow = kSmRow<DP>, kStages = kSmStages<WR>;
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kSmThreads, kSmCtas<WR>) prefix_small_kernel(c
     const PrefixPlan &pl = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp / WK, wk = warp % WK;
     const int D = d.head_dim, G = pl.G;
-    pdl_trigger();
+    start_of_items(second);
 
     // ---- the item: rows [row0, row0 + rows) of a run of queries, key tiles [t0, t1) of its list
     const int splits = kind == 0 ? pl.prefix_splits : pl.seq_splits, split = blockIdx.x % splits;
@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     const int b = static_cast<int>(t / d.max_q), j = static_cast<int>(t % d.max_q);
     const SeqRange r = seq_range(d, b);
     const bool live = inside && j < r.n_q;
+    pdl_trigger();
     pdl_wait();   // the parts are written
     const int64_t token = r.q0 + j;
     const int64_t row = token * d.n_heads + head, pitch = d.total_q * d.n_heads;
@@ -500,7 +501,7 @@ namespace {
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 template <typename T, int DP, int WR, int WK>
-cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s) {
+cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, bool second, cudaStream_t s) {
     if (items <= 0) return cudaSuccess;
     static bool configured[64] = {};
     int dev = 0;
@@ -514,10 +515,8 @@ cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, boo
     }
     cudaLaunchAttribute attr[2];
     int n_attr = 0;
-    if (early) {
-        attr[n_attr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n_attr++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[n_attr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n_attr++].val.programmaticStreamSerializationAllowed = 1;
     if (kind == 1 && a.p.cluster) {
         attr[n_attr].id = cudaLaunchAttributeClusterDimension;
         attr[n_attr].val.clusterDim.x = static_cast<unsigned>(a.p.seq_splits);
@@ -531,19 +530,19 @@ cudaError_t launch_small(const vitk::PrefixArgs &a, int kind, int64_t items, boo
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(n_attr);
-    return cudaLaunchKernelEx(&cfg, vitk::prefix_small_kernel<T, DP, WR, WK>, a, kind);
+    return cudaLaunchKernelEx(&cfg, vitk::prefix_small_kernel<T, DP, WR, WK>, a, kind, second);
 }
 
 template <typename T, int DP>
-cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool early, cudaStream_t s) {
-    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, early, s) : launch_small<T, DP, 2, 2>(a, kind, items, early, s);
+cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool second, cudaStream_t s) {
+    return m == 16 ? launch_small<T, DP, 1, 4>(a, kind, items, second, s) : launch_small<T, DP, 2, 2>(a, kind, items, second, s);
 }
 
 template <typename T>
-cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool early, cudaStream_t s) {
-    if (a.d.head_dim <= 64) return small<T, 64>(a, kind, m, items, early, s);
-    if (a.d.head_dim <= 80) return small<T, 80>(a, kind, m, items, early, s);
-    return small<T, 128>(a, kind, m, items, early, s);
+cudaError_t small(const vitk::PrefixArgs &a, int kind, int m, int64_t items, bool second, cudaStream_t s) {
+    if (a.d.head_dim <= 64) return small<T, 64>(a, kind, m, items, second, s);
+    if (a.d.head_dim <= 80) return small<T, 80>(a, kind, m, items, second, s);
+    return small<T, 128>(a, kind, m, items, second, s);
 }
 
 constexpr int kMaxCluster = 8;            // the portable cluster size
@@ -716,12 +715,12 @@ int join(const vitk::PrefixArgs &a, cudaStream_t s) {
     return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
-// early: the launch may start while the stream's previous kernel, this call's other items, drains
-int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, bool early, cudaStream_t s) {
+// second: the launch before is this call's other items, and runs beside these
+int run_items(const vitk::PrefixArgs &a, int kind, const Items &it, bool second, cudaStream_t s) {
     if (it.count <= 0) return VIT_OK;
-    if (it.m == kTcRows) return prefix_tc_launch(a, kind, it.count, early, s);
-    const cudaError_t e = a.d.dtype == VIT_DTYPE_BF16 ? small<__nv_bfloat16>(a, kind, it.m, it.count, early, s)
-                                                      : small<__half>(a, kind, it.m, it.count, early, s);
+    if (it.m == kTcRows) return prefix_tc_launch(a, kind, it.count, second, s);
+    const cudaError_t e = a.d.dtype == VIT_DTYPE_BF16 ? small<__nv_bfloat16>(a, kind, it.m, it.count, second, s)
+                                                      : small<__half>(a, kind, it.m, it.count, second, s);
     return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 
@@ -748,8 +747,8 @@ int prefix_attention_launch(const prefix_attention_desc &d, void *workspace, int
     // keys: the prefix first 27.7 us, the sequences first 30.0)
     int rc = VIT_OK;
     for (int i = 0; i < 2 && rc == VIT_OK; ++i) {
-        const bool early = i == 1 && pn.seq.count > 0 && pn.prefix.count > 0;
-        rc = (i == 0) == pn.prefix_first ? run_items(a, 0, pn.prefix, early, s) : run_items(a, 1, pn.seq, early, s);
+        const bool second = i == 1 && pn.seq.count > 0 && pn.prefix.count > 0;
+        rc = (i == 0) == pn.prefix_first ? run_items(a, 0, pn.prefix, second, s) : run_items(a, 1, pn.seq, second, s);
     }
     if (rc != VIT_OK || pn.p.parts == 1) return rc;
     return d.dtype == VIT_DTYPE_BF16 ? join<__nv_bfloat16>(a, s) : join<__half>(a, s);

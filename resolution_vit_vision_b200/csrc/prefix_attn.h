@@ -69,6 +69,14 @@ __device__ __forceinline__ SeqRange seq_range(const prefix_attention_desc &d, in
     return r;
 }
 
+// Both launches of items may start while the stream's kernel before drains. The first waits for it and lets the
+// next launch start only then; so the second, which that starts, finds everything before the call done.
+// (One sequence of 265 + 21 keys, call after call: 8.28 -> 6.73 us; 64 of 4113 + 517: 27.5 -> 25.8.)
+__device__ __forceinline__ void start_of_items(bool second) {
+    if (!second) pdl_wait();
+    pdl_trigger();
+}
+
 // The join waits for the last launch of items alone, so that launch may not be done before the one that it
 // started beside. One CTA sees to it, the last: if all waited, the early ones would keep their SMs from the
 // rest until then (256 sequences beside the prefix: 122 us a call).
@@ -89,6 +97,6 @@ namespace vith {
 // The tensor-core kernel (prefix_tc.cu) over `items` work items of `kind` (as prefix_small_kernel's),
 // kTcRows query rows each, in tiles of kTcKeys keys.
 constexpr int kTcRows = 256, kTcKeys = 80;
-// early: the launch may start while the stream's previous kernel drains.
-int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s);
+// second: the launch before is this call's other items.
+int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool second, cudaStream_t s);
 }  // namespace vith

@@ -64,7 +64,7 @@ template <typename T, int HV>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tpk, const __grid_constant__ CUtensorMap tpv,
                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                     const __grid_constant__ PrefixArgs a, int kind) {
+                     const __grid_constant__ PrefixArgs a, int kind, bool second) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr int kQTile = HV * kTcQBox, kTile = HV * kTcKBox;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // (descriptors, barrier addresses) in uniform registers, where the products read their operands
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int D = d.head_dim, G = pl.G;
-    pdl_trigger();
+    start_of_items(second);
 
     // ---- the item (as prefix_small_kernel's)
     const int splits = kind == 0 ? pl.prefix_splits : pl.seq_splits, split = blockIdx.x % splits;
@@ -464,7 +464,7 @@ int key_map(CUtensorMap *m, const prefix_attention_desc &d, const void *p, int64
 }
 
 template <typename T, int HV>
-cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kind, int64_t items, bool second, cudaStream_t s) {
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -475,17 +475,13 @@ cudaError_t launch(const CUtensorMap (&m)[4], const vitk::PrefixArgs &a, int kin
         if (e != cudaSuccess) return e;
         if (dev < 64) configured[dev] = true;
     }
-    if (early)
-        return launch_pdl(vitk::prefix_tc_kernel<T, HV>, dim3(static_cast<unsigned>(items)), dim3(vitk::kTcThreads),
-                          vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind);
-    vitk::prefix_tc_kernel<T, HV><<<static_cast<unsigned>(items), vitk::kTcThreads, vitk::kTcSmem<HV>, s>>>(
-        m[0], m[1], m[2], m[3], a, kind);
-    return cudaGetLastError();
+    return launch_pdl(vitk::prefix_tc_kernel<T, HV>, dim3(static_cast<unsigned>(items)), dim3(vitk::kTcThreads),
+                      vitk::kTcSmem<HV>, s, 1, m[0], m[1], m[2], m[3], a, kind, second);
 }
 
 }  // namespace
 
-int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool early, cudaStream_t s) {
+int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool second, cudaStream_t s) {
     if (items <= 0) return VIT_OK;
     const prefix_attention_desc &d = a.d;
     CUtensorMap m[4];
@@ -509,9 +505,9 @@ int prefix_tc_launch(const vitk::PrefixArgs &a, int kind, int64_t items, bool ea
     }
     cudaError_t e;
     if (d.dtype == VIT_DTYPE_BF16)
-        e = d.head_dim <= 64 ? launch<__nv_bfloat16, 1>(m, a, kind, items, early, s) : launch<__nv_bfloat16, 2>(m, a, kind, items, early, s);
+        e = d.head_dim <= 64 ? launch<__nv_bfloat16, 1>(m, a, kind, items, second, s) : launch<__nv_bfloat16, 2>(m, a, kind, items, second, s);
     else
-        e = d.head_dim <= 64 ? launch<__half, 1>(m, a, kind, items, early, s) : launch<__half, 2>(m, a, kind, items, early, s);
+        e = d.head_dim <= 64 ? launch<__half, 1>(m, a, kind, items, second, s) : launch<__half, 2>(m, a, kind, items, second, s);
     return e == cudaSuccess ? VIT_OK : VIT_ERR_CUDA;
 }
 

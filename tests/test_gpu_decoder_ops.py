@@ -305,3 +305,53 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0] * 2) and torch.equal(got[1], want[1] * 2)
     assert all(torch.equal(a, b) for a, b in zip(want[2:], got[2:]))
+
+
+@pytest.mark.parametrize("L", [1, 700])
+@pytest.mark.parametrize("graph", [False, True])
+def test_norm_calls_follow_what_the_stream_did_before(L, graph):
+    # launches may start early: operands written by slow kernels just before, results read by the next call,
+    # operands overwritten behind it
+    q, k, qw, kw, pos = _norm_case(L, 12, 2, 128, torch.bfloat16, 60)
+    ops = [q, k, qw, kw, pos]
+    kwargs = dict(sections=_secs(128))
+
+    def steps(q, k, qw, kw, pos, sync):
+        for _ in range(3):
+            nv.mrope_norm_apply(q, k, pos, qw, kw, q_out=q, k_out=k, **kwargs)
+            sync()
+        y = nv.mrope_norm_apply(q, k, pos, qw, kw, **kwargs)
+        sync()
+        g = nv.mrope_norm_grad(*y, q, k, pos, qw, kw, **kwargs)
+        sync()
+        return list(y) + list(g)
+    want = steps(*[t.clone() for t in ops], torch.cuda.synchronize)
+    slow = torch.zeros(64 << 20, dtype=torch.float32, device=DEV)
+    mine = [torch.zeros_like(t) for t in ops]
+
+    def chain():
+        slow.add_(1.0)
+        for a, b in zip(mine, ops):
+            a.copy_(b)
+        out = steps(*mine, lambda: None)
+        for a in mine:
+            a.zero_()
+        return out
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = chain()
+        s.synchronize()
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                got = chain()
+        for _ in range(5):
+            if graph:
+                for t in got:
+                    t.zero_()
+                g.replay()
+            else:
+                got = chain()
+        s.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -362,3 +362,45 @@ def test_prefix_and_sequences_on_the_tensor_cores_twice_at_once():
     torch.cuda.synchronize()
     for (a, cu), g in zip(cases, got):
         _check(a, cu, g)
+
+
+@pytest.mark.parametrize("B, Lp, H, Hk, D", [(1, 200, 12, 2, 128), (40, 700, 28, 4, 64), (3, 2000, 8, 1, 128)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_follow_what_the_stream_did_before(B, Lp, H, Hk, D, graph):
+    # launches may start early: inputs written by a slow kernel just before the call, each call's output the next
+    # one's queries, buffers overwritten behind it
+    a, cu = _case(50, B, 1, [30 + b for b in range(B)], Lp, H, Hk, D, "bf16")
+    want = [nv.prefix_attention(**a)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        want.append(nv.prefix_attention(**dict(a, q=want[-1][0])))
+        torch.cuda.synchronize()
+    slow = torch.zeros(64 << 20, dtype=torch.float32, device=DEV)
+    b = {n: torch.zeros_like(t) if isinstance(t, torch.Tensor) else t for n, t in a.items()}
+    got = [(torch.zeros_like(a["q"]), torch.zeros(B, H, device=DEV)) for _ in range(4)]
+
+    def chain():
+        slow.add_(1.0)
+        for n, t in a.items():
+            if isinstance(t, torch.Tensor):
+                b[n].copy_(t)
+        for i, (out, lse) in enumerate(got):
+            nv.prefix_attention(**dict(b, q=b["q"] if i == 0 else got[i - 1][0]), out=out, lse=lse)
+        for n, t in a.items():
+            if isinstance(t, torch.Tensor):
+                b[n].zero_()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        chain()
+        s.synchronize()
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                chain()
+        for _ in range(5):
+            for out, lse in got:
+                out.zero_()
+            g.replay() if graph else chain()
+        s.synchronize()
+    for (out, lse), (w, wl) in zip(got, want):
+        assert torch.equal(out, w) and torch.equal(lse, wl)
