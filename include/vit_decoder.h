@@ -17,6 +17,11 @@
  *
  * Conventions as in vit.h: device pointers unless marked HOST, bf16 row-major, asynchronous on
  * `stream`, argument errors returned before any launch, data errors written to dev_status.
+ * mrope_norm_apply, mrope_norm_grad and prefix_attention are launched with programmatic stream
+ * serialisation as the encoder's kernels are: they may start while the stream's previous kernel drains
+ * and wait for it to complete before they read or write any memory, and a kernel of the caller launched
+ * next with the same attribute has to wait (griddepcontrol.wait) before it touches what the call reads
+ * or writes.
  */
 #ifndef RESOLUTION_VIT_VISION_B200_VIT_DECODER_H
 #define RESOLUTION_VIT_VISION_B200_VIT_DECODER_H
@@ -143,12 +148,10 @@ typedef struct {
 /* workspace: prefix_attention_workspace(desc) bytes (host-only; 0 for a bad descriptor) of device
  * memory, 16-byte aligned, not shared with work that may run at the same time; it depends on sizes
  * alone, not on what cu_q and lens hold. The call's kernels are laid out for max_q queries and max_len
- * own keys of every sequence: bounds far above what cu_q and lens hold cost time. As with the encoder's
- * kernels, one that the caller launches next with programmatic stream serialisation may start early
- * and has to wait (griddepcontrol.wait) before it touches what the call reads or writes. Data errors (a length outside [0, max_len], query ranges that
- * do not start at 0, leave [0, total_q], run backwards or are longer than max_q) write VIT_ERR_LIMIT to dev_status (int32 [1] device, or
- * NULL); the values are clamped, nothing outside the buffers is touched, and the rows concerned
- * are not meaningful. A kernel wait that timed out writes VIT_ERR_TIMEOUT there. */
+ * own keys of every sequence: bounds far above what cu_q and lens hold cost time. Data errors (a length
+ * outside [0, max_len], query ranges that do not start at 0, leave [0, total_q], run backwards or are
+ * longer than max_q) write VIT_ERR_LIMIT to dev_status (int32 [1] device, or NULL); the values are
+ * clamped, nothing outside the buffers is touched, and the rows concerned are not meaningful. A kernel wait that timed out writes VIT_ERR_TIMEOUT there. */
 int64_t prefix_attention_workspace(const prefix_attention_desc *desc);
 int prefix_attention(const prefix_attention_desc *desc, void *workspace, int64_t workspace_bytes, int32_t *dev_status,
                      void *stream);

@@ -19,7 +19,7 @@
 // group's last lanes idle. Arithmetic is fp32 in pairs (fma.rn.f32x2), angles fp64, rounded once to the
 // element type on the way out. Measured: 40961 tokens of 28 + 4 heads of 128, fp16, 672 MB in 117-122 us, 5.5-
 // 5.7 TB/s (0.84-0.87 of the copy rate), 64% of issue slots; the gradient of 16411 tokens of 12 + 2 heads, fp32,
-// 353 MB in 61 us (0.88); of 3211 tokens of 28 + 4 heads, bf16, 79 MB in 27 us (start-up and instructions).
+// 353 MB in 60 us (0.90); of 3211 tokens of 28 + 4 heads, bf16, 79 MB in 25 us (start-up and instructions).
 #include <algorithm>
 #include <cmath>
 

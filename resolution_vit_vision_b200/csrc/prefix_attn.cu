@@ -633,7 +633,7 @@ Plan make_plan(const prefix_attention_desc &d) {
     for (int i = 0; i < all.n; ++i) {
         const Cut &c = all.cut[i];
         // up to eight short parts of small items join in a cluster's shared memory, with no part in HBM and no
-        // launch (one sequence, 265 shared keys: 10.2 -> 8.2 us); parts of nine tiles in clusters lost to more of
+        // launch (one sequence, 265 shared keys: 10.2 -> 8.2 us when it was made); parts of nine tiles in clusters lost to more of
         // them and a join (4 sequences, 4113 shared keys: 22.5 us against 18.5)
         const bool cluster = all.m != kTcRows && own > 0 && c.splits > 1 && c.splits <= kMaxCluster && c.tiles <= 4;
         const double us = c.us + (c.splits == 1 ? 0.0 : cluster ? 1.0 : c.splits * part_us + join_us);
