@@ -585,7 +585,9 @@ Kind kind(int64_t rows, int64_t runs, int64_t shared, int64_t own, int head_dim)
     const bool tc = k.m == kTcRows;
     k.ctas = tc ? 1 : k.m == 16 ? vitk::kSmCtas<1> : vitk::kSmCtas<2>;
     k.base = runs * ceil_div(rows, k.m);
-    const double tile_us = tc ? 1.0 : 0.7, start_us = tc ? 5.0 : 3.0;           // measured, latency of one item
+    // latency of an item, fitted to 17 mixes of 1 to 256 sequences, 200 to 16405 shared and 50 to 1000 own keys
+    // (0.7 for a small tile and 5 for a start on the tensor cores: 2.4% slower over all, 7% for 256 sequences)
+    const double tile_us = tc ? 1.0 : 0.9, start_us = tc ? 4.0 : 3.0;
     const int keys = tc ? kTcKeys : vitk::kSmKeys;
     const int tiles = std::max(1, ceil_div(shared, keys) + ceil_div(own, keys));   // no tile holds keys of both
     // small items are bound together by what the L2 gives the SMs, 5 MB per us; own keys count 0.6 of their bound
@@ -625,8 +627,8 @@ Plan make_plan(const prefix_attention_desc &d) {
     const bool own_keys = d.k != nullptr && d.max_len > 0;
     const int64_t max_rows = d.max_q * p.G, rows = d.total_q * p.G, runs = int64_t(d.n_seq) * d.n_kv_heads;
     const int64_t part_row_bytes = d.total_q * d.n_heads * d.head_dim * int64_t(sizeof(float)), own = own_keys ? d.max_len : 0;
-    // what a part costs (an fp32 row of o written and read, 4 MB per us) and the launch that joins them
-    const double part_us = part_row_bytes * 2 / 4.0e6, join_us = 4.0;
+    // what a part costs (an fp32 row of o written and read, 8 MB per us) and the launch that joins them
+    const double part_us = part_row_bytes * 2 / 8.0e6, join_us = 3.0;
     // Either every sequence's items go over its prefix and own keys in turn ...
     const Kind all = kind(max_rows, runs, d.prefix_len, own, d.head_dim);
     double best = 1e30;
